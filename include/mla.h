@@ -392,10 +392,48 @@ mla_status mla_normal_chunked(const mla_geom* geom, const mla_batch* batch, cons
                               const int32_t* seq_lens, const void* w_uk, const void* w_uv, int chunk_rows,
                               void* kv_chunk, void* state, void* o, float* lse, mla_stream_t stream);
 
+/*
+ * New tokens' queries and cache rows (the decoupled-RoPE layout of "MLA in full
+ * detail" and zdszero "MLA": queries [nope | rope], one shared rope key per token;
+ * DeepSeek-V2's norm of the compressed latent): query norm of each head, norm of the
+ * latent, position rotation and the write into the paged cache in one launch.
+ *   q  bf16 [N, H, 192], row (i, h) at q + i * q_token_stride + h * q_head_stride
+ *     (elements, multiples of 8, >= 0): 128 nope values, then 64 rope values;
+ *   kv bf16 [N, 576], row i at kv + i * kv_token_stride: 512 latent values before
+ *     their norm, then the 64 values of the key before its rotation;
+ *   q_weight bf16 [192] or NULL: each head's row becomes q / sqrt(mean(q^2) + eps) *
+ *     q_weight before the rotation; NULL leaves it as it is.  kv_weight bf16 [512] or
+ *     NULL: the same for the latent.  eps >= 0;
+ *   cos_sin float32 [max_pos, 64]: the 32 cosines, then the 32 sines of a position;
+ *   positions int32 [N], in [0, max_pos); tokens of a tree may share positions;
+ *   interleaved != 0: pair k is values (2k, 2k + 1) of the 64, else (k, k + 32); a
+ *     pair (a, b) becomes (a cos - b sin, b cos + a sin), in the same places;
+ *   slots int32 [N]: the physical row (block * 64 + offset) that token i's row
+ *     [latent 512 | rope 64] is written to; -1: none (a padding token).  The slots
+ *     other than -1 must differ: two tokens' rows in one slot leave a mixture.
+ * Writes q_nope bf16 [N, H, 128] and q_pe bf16 [N, H, 64] (as mla_absorb_q and
+ * mla_decode take them), which must not overlap the inputs, and the cache rows.  fp32
+ * arithmetic, each value rounded once to bf16.  A position outside [0, max_pos) leaves
+ * that token's outputs as they were; a slot outside the pool leaves the cache as it
+ * was; both are reported by mla_read_device_status (MLA_ERR_DEVICE_CHECK).
+ * mla_rope_append_fp8 writes 656-byte FP8 rows (cache_fp8 uint8 [num_blocks, 64, 656]):
+ * the bytes that mla_fp8_pack_cache makes of the row mla_rope_append writes.
+ */
+mla_status mla_rope_append(const mla_geom* geom, int N, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                           const void* kv, int64_t kv_token_stride, const void* q_weight, const void* kv_weight,
+                           float eps, const float* cos_sin, int max_pos, const int32_t* positions, int interleaved,
+                           const mla_cache* cache, const int32_t* slots, void* q_nope, void* q_pe,
+                           mla_stream_t stream);
+mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64_t q_token_stride,
+                               int64_t q_head_stride, const void* kv, int64_t kv_token_stride, const void* q_weight,
+                               const void* kv_weight, float eps, const float* cos_sin, int max_pos,
+                               const int32_t* positions, int interleaved, void* cache_fp8, int num_blocks,
+                               const int32_t* slots, void* q_nope, void* q_pe, mla_stream_t stream);
+
 /* Synchronise `stream`, then return the status word a kernel recorded in the
  * workspace (MLA_OK if none) and, if info != NULL, its detail word.  The
  * workspace-free kernels (absorption, un-absorption, the Normal arm, the gather
- * export) keep one status word per device, also returned (and cleared) here.
+ * export, the row append) keep one status word per device, also returned (and cleared) here.
  * With workspace = NULL the call reads that word and then the status and
  * detail words of mla_decode_noalloc's scratch on the current device, returns
  * the first that is set and clears it. */

@@ -62,6 +62,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
     I = ctypes.c_int
+    L64 = ctypes.c_int64
     G = ctypes.POINTER(mla_geom)
     C = ctypes.POINTER(mla_cache)
     Bt = ctypes.POINTER(mla_batch)
@@ -86,6 +87,8 @@ def _load() -> ctypes.CDLL:
         "mla_normal_chunk_bytes": (ctypes.c_size_t, [G, I, I]),
         "mla_normal_chunk_state_bytes": (ctypes.c_size_t, [G, Bt]),
         "mla_normal_chunked": (I, [G, Bt, P, P, C, P, I, P, P, P, I, P, P, P, P, P]),
+        "mla_rope_append": (I, [G, I, P, L64, L64, P, L64, P, P, ctypes.c_float, P, I, P, I, C, P, P, P, P]),
+        "mla_rope_append_fp8": (I, [G, I, P, L64, L64, P, L64, P, P, ctypes.c_float, P, I, P, I, P, I, P, P, P, P]),
         "mla_read_device_status": (I, [P, ctypes.POINTER(ctypes.c_int), P]),
         "mla_status_string": (ctypes.c_char_p, [I]),
         "mla_device_sm_count": (I, []),
@@ -102,6 +105,7 @@ EXPORTED = ("mla_workspace_size", "mla_plan", "mla_absorb_q", "mla_unabsorb_o", 
             "mla_sparse_workspace_size", "mla_decode_sparse", "mla_decode_fp8",
             "mla_split_merge", "mla_normal_rows_per_seq", "mla_normal_expanded_bytes", "mla_normal_expand",
             "mla_normal_attention", "mla_normal_chunk_bytes", "mla_normal_chunk_state_bytes", "mla_normal_chunked",
+            "mla_rope_append", "mla_rope_append_fp8",
             "mla_fp8_pack_cache", "mla_debug_gather", "mla_debug_set_wait_limit", "mla_read_device_status",
             "mla_status_string",
             "mla_device_sm_count")
@@ -281,6 +285,26 @@ def mla_normal_chunked(geom, batch, q_nope, q_pe, cache: mla_cache, block_table,
                                    ctypes.byref(cache), _ptr(block_table), bt_stride, _ptr(seq_lens), _ptr(w_uk),
                                    _ptr(w_uv), int(chunk_rows), _ptr(kv_chunk), _ptr(state), _ptr(o), _ptr(lse),
                                    _stream(stream))
+
+
+def mla_rope_append(geom, N: int, q, q_token_stride: int, q_head_stride: int, kv, kv_token_stride: int, q_weight,
+                    kv_weight, eps: float, cos_sin, max_pos: int, positions, interleaved, cache: mla_cache, slots,
+                    q_nope, q_pe, stream=None) -> int:
+    """Query norm, latent norm, rotation and the write of the new tokens' cache rows (strides in elements)."""
+    return _lib.mla_rope_append(ctypes.byref(geom), N, _ptr(q), q_token_stride, q_head_stride, _ptr(kv),
+                                kv_token_stride, _ptr(q_weight), _ptr(kv_weight), eps, _ptr(cos_sin), max_pos,
+                                _ptr(positions), int(interleaved), ctypes.byref(cache), _ptr(slots), _ptr(q_nope),
+                                _ptr(q_pe), _stream(stream))
+
+
+def mla_rope_append_fp8(geom, N: int, q, q_token_stride: int, q_head_stride: int, kv, kv_token_stride: int, q_weight,
+                        kv_weight, eps: float, cos_sin, max_pos: int, positions, interleaved, cache_fp8,
+                        num_blocks: int, slots, q_nope, q_pe, stream=None) -> int:
+    """The same into 656-byte FP8 rows (uint8 [num_blocks, 64, 656])."""
+    return _lib.mla_rope_append_fp8(ctypes.byref(geom), N, _ptr(q), q_token_stride, q_head_stride, _ptr(kv),
+                                    kv_token_stride, _ptr(q_weight), _ptr(kv_weight), eps, _ptr(cos_sin), max_pos,
+                                    _ptr(positions), int(interleaved), _ptr(cache_fp8), num_blocks, _ptr(slots),
+                                    _ptr(q_nope), _ptr(q_pe), _stream(stream))
 
 
 def mla_read_device_status(workspace, stream=None) -> tuple[int, int]:

@@ -420,6 +420,66 @@ mla_status mla_normal_chunked(const mla_geom* geom, const mla_batch* batch, cons
                                            static_cast<__nv_bfloat16*>(o), lse, (cudaStream_t)stream));
 }
 
+// Shared by the two forms of the append: everything but the cache (fills c).
+static mla_status append_args(const mla_geom* geom, int N, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                              const void* kv, int64_t kv_token_stride, const void* q_weight, const void* kv_weight,
+                              float eps, const float* cos_sin, int max_pos, const int32_t* positions, int interleaved,
+                              const int32_t* slots, void* q_nope, void* q_pe, AppendCall* c) {
+  const mla_status s = check_geom(geom);
+  if (s != MLA_OK) return s;
+  if (N < 0 || !(eps >= 0.f) || max_pos < 1) return MLA_ERR_ARG;
+  if (N == 0) return MLA_OK;
+  if (!q || !kv || !cos_sin || !positions || !slots || !q_nope || !q_pe) return MLA_ERR_ARG;
+  if (q_token_stride < 0 || q_head_stride < 0 || kv_token_stride < 0) return MLA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(q_weight) || !aligned16(kv_weight) || !aligned16(cos_sin) ||
+      !aligned16(positions) || !aligned16(slots) || !aligned16(q_nope) || !aligned16(q_pe))
+    return MLA_ERR_ALIGN;
+  if (q_token_stride % 8 != 0 || q_head_stride % 8 != 0 || kv_token_stride % 8 != 0) return MLA_ERR_ALIGN;
+  if ((long long)N * (geom->H + 1) >= (1LL << 31)) return MLA_ERR_SHAPE;
+  c->N = N; c->H = geom->H;
+  c->q = static_cast<const __nv_bfloat16*>(q); c->q_token = q_token_stride; c->q_head = q_head_stride;
+  c->kv = static_cast<const __nv_bfloat16*>(kv); c->kv_token = kv_token_stride;
+  c->q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  c->kv_weight = static_cast<const __nv_bfloat16*>(kv_weight);
+  c->eps = eps; c->cos_sin = cos_sin; c->max_pos = max_pos; c->positions = positions; c->slots = slots;
+  c->interleaved = interleaved != 0;
+  c->q_nope = static_cast<__nv_bfloat16*>(q_nope); c->q_pe = static_cast<__nv_bfloat16*>(q_pe);
+  c->rows_fp8 = nullptr;
+  return MLA_OK;
+}
+
+mla_status mla_rope_append(const mla_geom* geom, int N, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                           const void* kv, int64_t kv_token_stride, const void* q_weight, const void* kv_weight,
+                           float eps, const float* cos_sin, int max_pos, const int32_t* positions, int interleaved,
+                           const mla_cache* cache, const int32_t* slots, void* q_nope, void* q_pe,
+                           mla_stream_t stream) {
+  AppendCall c;
+  mla_status s = append_args(geom, N, q, q_token_stride, q_head_stride, kv, kv_token_stride, q_weight, kv_weight, eps,
+                             cos_sin, max_pos, positions, interleaved, slots, q_nope, q_pe, &c);
+  if (s != MLA_OK || N == 0) return s;
+  if ((s = check_cache(cache, &c.cv)) != MLA_OK) return s;
+  if ((long long)c.cv.num_blocks * kPage >= (1LL << 31)) return MLA_ERR_SHAPE;
+  return cuda_status(launch_rope_append(c, (cudaStream_t)stream));
+}
+
+mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64_t q_token_stride,
+                               int64_t q_head_stride, const void* kv, int64_t kv_token_stride, const void* q_weight,
+                               const void* kv_weight, float eps, const float* cos_sin, int max_pos,
+                               const int32_t* positions, int interleaved, void* cache_fp8, int num_blocks,
+                               const int32_t* slots, void* q_nope, void* q_pe, mla_stream_t stream) {
+  AppendCall c;
+  const mla_status s = append_args(geom, N, q, q_token_stride, q_head_stride, kv, kv_token_stride, q_weight, kv_weight,
+                                   eps, cos_sin, max_pos, positions, interleaved, slots, q_nope, q_pe, &c);
+  if (s != MLA_OK || N == 0) return s;
+  if (!cache_fp8 || num_blocks < 1) return MLA_ERR_ARG;
+  if (!aligned16(cache_fp8)) return MLA_ERR_ALIGN;
+  if ((long long)num_blocks * kPage >= (1LL << 31)) return MLA_ERR_SHAPE;
+  c.cv = CacheView{};
+  c.cv.num_blocks = num_blocks;
+  c.rows_fp8 = static_cast<unsigned char*>(cache_fp8);
+  return cuda_status(launch_rope_append(c, (cudaStream_t)stream));
+}
+
 mla_status mla_read_device_status(const void* workspace, int* info, mla_stream_t stream) {
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
   if (info) *info = 0;

@@ -121,6 +121,25 @@ cudaError_t launch_absorb_sm103(const __nv_bfloat16* q_nope, const __nv_bfloat16
 cudaError_t launch_unabsorb_sm103(const __nv_bfloat16* o_lat, const __nv_bfloat16* w_uv, __nv_bfloat16* o,
                                   int BT, int H, cudaStream_t st);
 int* bmm_status_ptr();
+// New tokens' queries and cache rows (mla_rope_append): rows_fp8 != null writes FP8 rows
+// of a pool of cv.num_blocks blocks, else cv is the bf16 pool.
+struct AppendCall {
+  int N, H;
+  const __nv_bfloat16* q;
+  int64_t q_token, q_head;
+  const __nv_bfloat16* kv;
+  int64_t kv_token;
+  const __nv_bfloat16 *q_weight, *kv_weight;
+  float eps;
+  const float* cos_sin;
+  int max_pos;
+  const int32_t *positions, *slots;
+  bool interleaved;
+  CacheView cv;
+  unsigned char* rows_fp8;
+  __nv_bfloat16 *q_nope, *q_pe;
+};
+cudaError_t launch_rope_append(const AppendCall& c, cudaStream_t st);
 int64_t normal_rows_per_seq(int max_pages);
 cudaError_t launch_normal_expand(const mla_geom* g, const CacheView& cv, const int32_t* block_table, int bt_stride,
                                  const int32_t* seq_lens, int B, int max_pages, const __nv_bfloat16* w_uk,
