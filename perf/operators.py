@@ -9,7 +9,8 @@ A step with drafted tokens has four parts, and each is an operator here:
   verify   acceptance of the drafted tokens against the target's probabilities, from given random
            numbers (mla_verify_tree)
   pages    the cache afterwards: accepted rows moved together (mla_cache_compact); sequences released
-           and forked, full pages shared and the last page copied (mla_pages_resize, mla_pages_fork)
+           and forked, full pages shared and the last page copied (mla_pages_resize, mla_pages_fork,
+           mla_cache_copy)
 
 With ``own`` false, ``run`` computes a case in plain torch operations (32 bits; 64 where a decision
 lies next to a border); with ``own`` true it calls the library.
@@ -249,8 +250,7 @@ def _prepare_fork(case, rng, g):
     keep = lens.copy()
     keep[dst] = 0
     return dict(pool=_normal(g, (nb, PAGE, D_K), 0.1), block_table=_dev(bt), seq_lens=_dev(lens), keep_lens=_dev(keep),
-                refs=_dev(refs), src=_dev(src.astype(np.int32)), dst=_dev(dst.astype(np.int32)),
-                fork_status=torch.empty((B // 2,), dtype=torch.int32, device=DEV))
+                refs=_dev(refs), src=_dev(src.astype(np.int32)), dst=_dev(dst.astype(np.int32)))
 
 
 # --------------------------------------------------------------------------- the library's own handles
@@ -277,7 +277,9 @@ def _handles_compact(s, L):
     s["cache"] = L.cache_from_pool(s["pool"])
 
 
-_handles_fork = _handles_compact
+def _handles_fork(s, L):
+    s["cache"] = L.cache_from_pool(s["pool"])
+    s["copies"] = torch.empty((3, s["case"]["B"] // 2), dtype=torch.int32, device=DEV)
 
 
 # ------------------------------------------------------------------------------------------------ run
@@ -330,8 +332,9 @@ def _own_fork(s):
     nb = s["pool"].shape[0]
     L.check(L.mla_pages_resize(s["refs"], nb, bt, bt.shape[1], bt.shape[1], s["seq_lens"], s["keep_lens"], B,
                                s["seq_lens"]), "mla_pages_resize")
-    L.check(L.mla_pages_fork(s["cache"], s["refs"], bt, bt.shape[1], bt.shape[1], s["seq_lens"], B, s["src"], s["dst"],
-                             B // 2, s["fork_status"]), "mla_pages_fork")
+    L.check(L.mla_pages_fork(s["refs"], nb, bt, bt.shape[1], bt.shape[1], s["seq_lens"], B, s["src"], s["dst"], B // 2,
+                             s["copies"]), "mla_pages_fork")
+    L.check(L.mla_cache_copy(s["cache"], s["copies"], B // 2), "mla_cache_copy")
     return bt, s["refs"], s["seq_lens"], s["pool"]
 
 
