@@ -82,6 +82,9 @@ typedef enum {
   MLA_ERR_TIMEOUT = -8       /* (device) a bounded wait ran out */
 } mla_status;
 
+/* Element types of arrays that come in more than one. */
+typedef enum { MLA_DTYPE_F32 = 0, MLA_DTYPE_BF16 = 1 } mla_dtype;
+
 typedef struct {
   int H;               /* query heads (DeepSeek-V2-Lite 16, V3 128) */
   int d_lat;           /* kv_lora_rank, must be 512 */
@@ -430,10 +433,113 @@ mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64
                                const int32_t* positions, int interleaved, void* cache_fp8, int num_blocks,
                                const int32_t* slots, void* q_nope, void* q_pe, mla_stream_t stream);
 
+/*
+ * Verification of drafted tokens against the target's probabilities, from given
+ * random numbers, so that the emitted tokens are distributed as the target's
+ * (rejection sampling with residuals).  A sequence's drafts form a tree (a chain is
+ * a tree without branches): node 0 is the last token already decided, node t > 0
+ * holds the drafted token tokens[b, t] and hangs on parents[b, t] < t; parents[b, 0]
+ * and tokens[b, 0] are not used.  1 <= T <= 1024 nodes per sequence, of which the
+ * first node_lens[b] count (node_lens NULL: all T; 0: nothing is decided).
+ *   target_probs, draft_probs: row (b, t) at base + (b * T + t) * row_stride elements
+ *     (fp32 or bf16 by dtype; row_stride >= V, rows 16-byte aligned): the target's
+ *     probabilities of the token after node t, and those that node t's children were
+ *     drawn from (independent draws; not read at nodes without children).  draft_probs
+ *     NULL: each draft is taken as certain (a point mass), as the likeliest tokens of a
+ *     drafter are.  Negative values and NaN count as 0; rows need not sum to 1 exactly.
+ *   u_accept float32 [B, T] (node t's number), u_sample float32 [B]: in [0, 1).
+ * Rule: from cur = 0, the children of cur are tried in index order.  With p, q the rows
+ * of cur, k of its children refused so far, R_k = max(p - C_k q, 0), C_0 = 0, Z_0 = 1,
+ * C_{k+1} = C_k + Z_k, Z_k = sum R_k: child x is accepted, and becomes cur, when
+ * R_k(x) > 0 and u q(x) Z_k < R_k(x).  Point masses: R_k is p without the tokens
+ * refused here, Z_k = 1 - their p, and x is accepted when R_k(x) > 0 and u Z_k < R_k(x).
+ * When no child is left the next token is the first x with R_k(0) + ... + R_k(x) >
+ * u_sample * sum R_k (the last x with R_k(x) > 0 if there is none); where R_k is 0
+ * everywhere, p takes its place, and where p is too, the token is -1.  Products and
+ * sums are fp64.
+ * Outputs (int32): accept_len[b] = accepted nodes, node 0 included (>= 1; 0 where
+ * node_lens[b] = 0); accept_idx[b, 0 .. accept_len) = their indices, increasing;
+ * out_tokens[b, 0 .. accept_len) = the tokens decided: those of the accepted nodes
+ * after node 0, then the next token; -1 past accept_len in both.
+ * A node whose parent is not an earlier node, or whose token is outside [0, V), is
+ * passed over, a node count outside [0, T] counts as 0; both are reported by
+ * mla_read_device_status (MLA_ERR_DEVICE_CHECK).
+ */
+mla_status mla_verify_tree(int B, int T, int V, const void* target_probs, const void* draft_probs, mla_dtype dtype,
+                           int64_t row_stride, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* node_lens, const float* u_accept, const float* u_sample,
+                           int32_t* accept_len, int32_t* accept_idx, int32_t* out_tokens, mla_stream_t stream);
+
+/*
+ * Pages of the cache after a step ("M5.8" 0x05: pages through a block table, held by
+ * more than one sequence when prefixes are shared).  Rows and pages move in one
+ * layer's pool (mla_cache_*: call once per layer); who holds which block is kept once,
+ * next to the block table (mla_pages_*):
+ *   refs int32 [num_blocks]: how many block-table entries hold block k; 0: free.  All
+ *     zero at first.  Sequence b of length L holds the blocks of its first
+ *     ceil(L / 64) table entries; entries past those are -1.
+ * What is allocated is the lowest free blocks, in order: results depend on the
+ * arguments alone.  seq_lens, cur_lens, new_lens in [0, 64 max_pages]; bt_stride >=
+ * max_pages.  Device-side problems are reported by mla_read_device_status
+ * (MLA_ERR_DEVICE_CHECK).
+ */
+
+/* The accepted nodes' rows moved together (after mla_verify_tree): sequence b has
+ * seq_lens[b] rows, the last n_b = node_lens[b] (NULL: T) of them its tree's nodes;
+ * row S_b - n_b + accept_idx[b, i] moves to S_b - n_b + i for i < accept_len[b], and
+ * new_lens[b] = S_b - n_b + accept_len[b] (new_lens is none of the inputs).  The rows
+ * in between keep what they held.  accept_idx int32 [B, T], increasing strictly; T <=
+ * 1024.  The nodes' pages must be the sequence's own.  A sequence with a bad length,
+ * count, index or block id is reported and left as it was, new_lens[b] = seq_lens[b].
+ * Give back the pages past the new lengths with mla_pages_resize. */
+mla_status mla_cache_compact(const mla_cache* cache, const int32_t* block_table, int bt_stride, int max_pages,
+                             const int32_t* seq_lens, const int32_t* node_lens, const int32_t* accept_len,
+                             const int32_t* accept_idx, int B, int T, int32_t* new_lens, mla_stream_t stream);
+mla_status mla_cache_compact_fp8(void* cache_fp8, int num_blocks, const int32_t* block_table, int bt_stride,
+                                 int max_pages, const int32_t* seq_lens, const int32_t* node_lens,
+                                 const int32_t* accept_len, const int32_t* accept_idx, int B, int T,
+                                 int32_t* new_lens, mla_stream_t stream);
+
+/* Sequences shortened and lengthened: sequence b goes from cur_lens[b] rows to
+ * new_lens[b].  Pages past the new length are given back (all of them with new_lens[b]
+ * = 0), their table entries become -1; then pages are allocated for the longer ones,
+ * sequence by sequence.  got_lens[b] (may be cur_lens or new_lens) is new_lens[b], or,
+ * where the free blocks ran out (reported), 64 times the pages b holds.  A length out
+ * of range is reported and leaves the sequence as it was (got_lens[b] = cur_lens[b]); a
+ * table entry outside the pool, or a block that nobody holds, is reported and given
+ * back as far as it goes.  B <= 8192.
+ * A sequence shortened into a page that others hold too must get a page of its own
+ * before rows are written behind its end: mla_pages_fork from itself. */
+mla_status mla_pages_resize(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
+                            const int32_t* cur_lens, const int32_t* new_lens, int B, int32_t* got_lens,
+                            mla_stream_t stream);
+
+/* Sequences forked: for f < F, sequence dst[f] becomes a fork of src[f]: its table row
+ * takes src's full pages (one more holder each) and, where src's last page is partly
+ * filled, a newly allocated block for a copy of it; seq_lens[dst[f]] = seq_lens[src[f]].
+ * What dst held before must have been given back.  src[f] = dst[f] gives the sequence a
+ * last page of its own where others hold it too.  A src may occur many times, a dst
+ * once, and a src is no other fork's dst.  copies int32 [3, F]: from block, to block
+ * and filled rows of the page to copy (rows 0: none), for mla_cache_copy of each layer.
+ * A fork that breaks these rules, or for which no free block is left (by order of f),
+ * is reported, changes nothing and gets from = -2, rows = 0; a full page whose table
+ * entry is outside the pool is reported, and the entry taken over as it is.
+ * B <= 65536, F <= 4096. */
+mla_status mla_pages_fork(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
+                          int32_t* seq_lens, int B, const int32_t* src, const int32_t* dst, int F, int32_t* copies,
+                          mla_stream_t stream);
+
+/* Pages copied within a pool: the first copies[2, i] rows (0 .. 64) of block
+ * copies[0, i] to block copies[1, i], i < n; copies int32 [3, n].  No block may be
+ * written twice, or written and read.  A block outside the pool, or a row count out of
+ * range, is reported and skipped; with a count of 0 nothing is looked at. */
+mla_status mla_cache_copy(const mla_cache* cache, const int32_t* copies, int n, mla_stream_t stream);
+mla_status mla_cache_copy_fp8(void* cache_fp8, int num_blocks, const int32_t* copies, int n, mla_stream_t stream);
+
 /* Synchronise `stream`, then return the status word a kernel recorded in the
  * workspace (MLA_OK if none) and, if info != NULL, its detail word.  The
  * workspace-free kernels (absorption, un-absorption, the Normal arm, the gather
- * export, the row append) keep one status word per device, also returned (and cleared) here.
+ * export, the row append, the verification, the page calls) keep one status word per device, also returned (and cleared) here.
  * With workspace = NULL the call reads that word and then the status and
  * detail words of mla_decode_noalloc's scratch on the current device, returns
  * the first that is set and clears it. */

@@ -25,6 +25,9 @@ MLA_ERR_CUDA = -6
 MLA_ERR_DEVICE_CHECK = -7
 MLA_ERR_TIMEOUT = -8
 
+MLA_DTYPE_F32 = 0
+MLA_DTYPE_BF16 = 1
+
 # plan header word indices (include/mla.h)
 HDR = dict(MAGIC=0, B=1, T=2, H=3, CAUSAL=4, NUM_GROUPS=5, NUM_SEGMENTS=6, NUM_RANGES=7, NUM_PARTIALS=8,
            NUM_MERGE=9, SEQ_HASH=10, ERROR=11, ERROR_INFO=12, PAGES_PER_RANGE=13, NUM_SLOTS=14, OVERRIDE=15,
@@ -89,6 +92,13 @@ def _load() -> ctypes.CDLL:
         "mla_normal_chunked": (I, [G, Bt, P, P, C, P, I, P, P, P, I, P, P, P, P, P]),
         "mla_rope_append": (I, [G, I, P, L64, L64, P, L64, P, P, ctypes.c_float, P, I, P, I, C, P, P, P, P]),
         "mla_rope_append_fp8": (I, [G, I, P, L64, L64, P, L64, P, P, ctypes.c_float, P, I, P, I, P, I, P, P, P, P]),
+        "mla_verify_tree": (I, [I, I, I, P, P, I, L64, P, P, P, P, P, P, P, P, P]),
+        "mla_cache_compact": (I, [C, P, I, I, P, P, P, P, I, I, P, P]),
+        "mla_cache_compact_fp8": (I, [P, I, P, I, I, P, P, P, P, I, I, P, P]),
+        "mla_pages_resize": (I, [P, I, P, I, I, P, P, I, P, P]),
+        "mla_pages_fork": (I, [P, I, P, I, I, P, I, P, P, I, P, P]),
+        "mla_cache_copy": (I, [C, P, I, P]),
+        "mla_cache_copy_fp8": (I, [P, I, P, I, P]),
         "mla_read_device_status": (I, [P, ctypes.POINTER(ctypes.c_int), P]),
         "mla_status_string": (ctypes.c_char_p, [I]),
         "mla_device_sm_count": (I, []),
@@ -105,7 +115,9 @@ EXPORTED = ("mla_workspace_size", "mla_plan", "mla_absorb_q", "mla_unabsorb_o", 
             "mla_sparse_workspace_size", "mla_decode_sparse", "mla_decode_fp8",
             "mla_split_merge", "mla_normal_rows_per_seq", "mla_normal_expanded_bytes", "mla_normal_expand",
             "mla_normal_attention", "mla_normal_chunk_bytes", "mla_normal_chunk_state_bytes", "mla_normal_chunked",
-            "mla_rope_append", "mla_rope_append_fp8",
+            "mla_rope_append", "mla_rope_append_fp8", "mla_verify_tree",
+            "mla_cache_compact", "mla_cache_compact_fp8", "mla_pages_resize", "mla_pages_fork", "mla_cache_copy",
+            "mla_cache_copy_fp8",
             "mla_fp8_pack_cache", "mla_debug_gather", "mla_debug_set_wait_limit", "mla_read_device_status",
             "mla_status_string",
             "mla_device_sm_count")
@@ -305,6 +317,52 @@ def mla_rope_append_fp8(geom, N: int, q, q_token_stride: int, q_head_stride: int
                                     kv_token_stride, _ptr(q_weight), _ptr(kv_weight), eps, _ptr(cos_sin), max_pos,
                                     _ptr(positions), int(interleaved), _ptr(cache_fp8), num_blocks, _ptr(slots),
                                     _ptr(q_nope), _ptr(q_pe), _stream(stream))
+
+
+def mla_verify_tree(B: int, T: int, V: int, target_probs, draft_probs, dtype: int, row_stride: int, tokens, parents,
+                    node_lens, u_accept, u_sample, accept_len, accept_idx, out_tokens, stream=None) -> int:
+    """Accept or refuse drafted tokens, and draw the token after them (draft_probs None: point masses)."""
+    return _lib.mla_verify_tree(B, T, V, _ptr(target_probs), _ptr(draft_probs), dtype, row_stride, _ptr(tokens),
+                                _ptr(parents), _ptr(node_lens), _ptr(u_accept), _ptr(u_sample), _ptr(accept_len),
+                                _ptr(accept_idx), _ptr(out_tokens), _stream(stream))
+
+
+def mla_cache_compact(cache: mla_cache, block_table, bt_stride: int, max_pages: int, seq_lens, node_lens, accept_len,
+                      accept_idx, B: int, T: int, new_lens, stream=None) -> int:
+    """Move the accepted nodes' rows together behind each sequence's prefix."""
+    return _lib.mla_cache_compact(ctypes.byref(cache), _ptr(block_table), bt_stride, max_pages, _ptr(seq_lens),
+                                  _ptr(node_lens), _ptr(accept_len), _ptr(accept_idx), B, T, _ptr(new_lens),
+                                  _stream(stream))
+
+
+def mla_cache_compact_fp8(cache_fp8, num_blocks: int, block_table, bt_stride: int, max_pages: int, seq_lens, node_lens,
+                          accept_len, accept_idx, B: int, T: int, new_lens, stream=None) -> int:
+    return _lib.mla_cache_compact_fp8(_ptr(cache_fp8), num_blocks, _ptr(block_table), bt_stride, max_pages,
+                                      _ptr(seq_lens), _ptr(node_lens), _ptr(accept_len), _ptr(accept_idx), B, T,
+                                      _ptr(new_lens), _stream(stream))
+
+
+def mla_pages_resize(refs, num_blocks: int, block_table, bt_stride: int, max_pages: int, cur_lens, new_lens, B: int,
+                     got_lens, stream=None) -> int:
+    """Give back the pages past shorter lengths, allocate those of longer ones."""
+    return _lib.mla_pages_resize(_ptr(refs), num_blocks, _ptr(block_table), bt_stride, max_pages, _ptr(cur_lens),
+                                 _ptr(new_lens), B, _ptr(got_lens), _stream(stream))
+
+
+def mla_pages_fork(refs, num_blocks: int, block_table, bt_stride: int, max_pages: int, seq_lens, B: int, src, dst,
+                   F: int, copies, stream=None) -> int:
+    """Fork sequences (full pages shared); copies [3, F] lists the last pages to copy with mla_cache_copy."""
+    return _lib.mla_pages_fork(_ptr(refs), num_blocks, _ptr(block_table), bt_stride, max_pages, _ptr(seq_lens), B,
+                               _ptr(src), _ptr(dst), F, _ptr(copies), _stream(stream))
+
+
+def mla_cache_copy(cache: mla_cache, copies, n: int, stream=None) -> int:
+    """Copy pages of a pool: copies int32 [3, n] (from block, to block, rows)."""
+    return _lib.mla_cache_copy(ctypes.byref(cache), _ptr(copies), n, _stream(stream))
+
+
+def mla_cache_copy_fp8(cache_fp8, num_blocks: int, copies, n: int, stream=None) -> int:
+    return _lib.mla_cache_copy_fp8(_ptr(cache_fp8), num_blocks, _ptr(copies), n, _stream(stream))
 
 
 def mla_read_device_status(workspace, stream=None) -> tuple[int, int]:

@@ -420,6 +420,18 @@ mla_status mla_normal_chunked(const mla_geom* geom, const mla_batch* batch, cons
                                            static_cast<__nv_bfloat16*>(o), lse, (cudaStream_t)stream));
 }
 
+// An FP8 pool as a view (only its block count is used).
+static mla_status check_fp8_pool(const void* cache_fp8, int num_blocks, CacheView* cv) {
+  if (!cache_fp8 || num_blocks < 1) return MLA_ERR_ARG;
+  if (!aligned16(cache_fp8)) return MLA_ERR_ALIGN;
+  *cv = CacheView{};
+  cv->num_blocks = num_blocks;
+  return MLA_OK;
+}
+static mla_status check_rows32(const CacheView& cv) {   // physical rows as 32-bit numbers
+  return (long long)cv.num_blocks * kPage >= (1LL << 31) ? MLA_ERR_SHAPE : MLA_OK;
+}
+
 // Shared by the two forms of the append: everything but the cache (fills c).
 static mla_status append_args(const mla_geom* geom, int N, const void* q, int64_t q_token_stride, int64_t q_head_stride,
                               const void* kv, int64_t kv_token_stride, const void* q_weight, const void* kv_weight,
@@ -458,7 +470,7 @@ mla_status mla_rope_append(const mla_geom* geom, int N, const void* q, int64_t q
                              cos_sin, max_pos, positions, interleaved, slots, q_nope, q_pe, &c);
   if (s != MLA_OK || N == 0) return s;
   if ((s = check_cache(cache, &c.cv)) != MLA_OK) return s;
-  if ((long long)c.cv.num_blocks * kPage >= (1LL << 31)) return MLA_ERR_SHAPE;
+  if ((s = check_rows32(c.cv)) != MLA_OK) return s;
   return cuda_status(launch_rope_append(c, (cudaStream_t)stream));
 }
 
@@ -468,16 +480,133 @@ mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64
                                const int32_t* positions, int interleaved, void* cache_fp8, int num_blocks,
                                const int32_t* slots, void* q_nope, void* q_pe, mla_stream_t stream) {
   AppendCall c;
-  const mla_status s = append_args(geom, N, q, q_token_stride, q_head_stride, kv, kv_token_stride, q_weight, kv_weight,
+  mla_status s = append_args(geom, N, q, q_token_stride, q_head_stride, kv, kv_token_stride, q_weight, kv_weight,
                                    eps, cos_sin, max_pos, positions, interleaved, slots, q_nope, q_pe, &c);
   if (s != MLA_OK || N == 0) return s;
-  if (!cache_fp8 || num_blocks < 1) return MLA_ERR_ARG;
-  if (!aligned16(cache_fp8)) return MLA_ERR_ALIGN;
-  if ((long long)num_blocks * kPage >= (1LL << 31)) return MLA_ERR_SHAPE;
-  c.cv = CacheView{};
-  c.cv.num_blocks = num_blocks;
+  if ((s = check_fp8_pool(cache_fp8, num_blocks, &c.cv)) != MLA_OK) return s;
+  if ((s = check_rows32(c.cv)) != MLA_OK) return s;
   c.rows_fp8 = static_cast<unsigned char*>(cache_fp8);
   return cuda_status(launch_rope_append(c, (cudaStream_t)stream));
+}
+
+mla_status mla_verify_tree(int B, int T, int V, const void* target_probs, const void* draft_probs, mla_dtype dtype,
+                           int64_t row_stride, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* node_lens, const float* u_accept, const float* u_sample,
+                           int32_t* accept_len, int32_t* accept_idx, int32_t* out_tokens, mla_stream_t stream) {
+  if (B < 0 || T < 1 || V < 1 || row_stride < V) return MLA_ERR_ARG;
+  if (dtype != MLA_DTYPE_F32 && dtype != MLA_DTYPE_BF16) return MLA_ERR_ARG;
+  if (T > kMaxTreeNodes || V > (1 << 30)) return MLA_ERR_SHAPE;
+  if (B == 0) return MLA_OK;
+  if (!target_probs || !tokens || !parents || !u_accept || !u_sample || !accept_len || !accept_idx || !out_tokens)
+    return MLA_ERR_ARG;
+  if (!aligned16(target_probs) || !aligned16(draft_probs) || !aligned16(tokens) || !aligned16(parents) ||
+      !aligned16(node_lens) || !aligned16(u_accept) || !aligned16(u_sample) || !aligned16(accept_len) ||
+      !aligned16(accept_idx) || !aligned16(out_tokens))
+    return MLA_ERR_ALIGN;
+  if ((row_stride * (dtype == MLA_DTYPE_BF16 ? 2 : 4)) % 16 != 0) return MLA_ERR_ALIGN;
+  const VerifyCall c{B, T, V, target_probs, draft_probs, dtype == MLA_DTYPE_BF16, row_stride, tokens, parents,
+                     node_lens, u_accept, u_sample, accept_len, accept_idx, out_tokens};
+  return cuda_status(launch_verify_tree(c, (cudaStream_t)stream));
+}
+
+static mla_status cache_compact(const CacheView& cv, void* rows_fp8, const int32_t* block_table, int bt_stride,
+                                int max_pages, const int32_t* seq_lens, const int32_t* node_lens,
+                                const int32_t* accept_len, const int32_t* accept_idx, int B, int T, int32_t* new_lens,
+                                mla_stream_t stream) {
+  if (B < 0 || T < 1 || max_pages < 1 || bt_stride < max_pages) return MLA_ERR_ARG;
+  if (T > kMaxTreeNodes || max_pages >= (1 << 25)) return MLA_ERR_SHAPE;
+  if (B == 0) return MLA_OK;
+  if (!block_table || !seq_lens || !accept_len || !accept_idx || !new_lens) return MLA_ERR_ARG;
+  if (new_lens == seq_lens || new_lens == node_lens || new_lens == accept_len) return MLA_ERR_ARG;
+  if (!aligned16(block_table) || !aligned16(seq_lens) || !aligned16(node_lens) || !aligned16(accept_len) ||
+      !aligned16(accept_idx) || !aligned16(new_lens))
+    return MLA_ERR_ALIGN;
+  const mla_status s = check_rows32(cv);
+  if (s != MLA_OK) return s;
+  return cuda_status(launch_cache_compact(cv, static_cast<unsigned char*>(rows_fp8), block_table, bt_stride, max_pages,
+                                          seq_lens, node_lens, accept_len, accept_idx, B, T, new_lens,
+                                          (cudaStream_t)stream));
+}
+
+mla_status mla_cache_compact(const mla_cache* cache, const int32_t* block_table, int bt_stride, int max_pages,
+                             const int32_t* seq_lens, const int32_t* node_lens, const int32_t* accept_len,
+                             const int32_t* accept_idx, int B, int T, int32_t* new_lens, mla_stream_t stream) {
+  CacheView cv;
+  const mla_status s = check_cache(cache, &cv);
+  if (s != MLA_OK) return s;
+  return cache_compact(cv, nullptr, block_table, bt_stride, max_pages, seq_lens, node_lens, accept_len, accept_idx, B,
+                       T, new_lens, stream);
+}
+
+mla_status mla_cache_compact_fp8(void* cache_fp8, int num_blocks, const int32_t* block_table, int bt_stride,
+                                 int max_pages, const int32_t* seq_lens, const int32_t* node_lens,
+                                 const int32_t* accept_len, const int32_t* accept_idx, int B, int T, int32_t* new_lens,
+                                 mla_stream_t stream) {
+  CacheView cv;
+  const mla_status s = check_fp8_pool(cache_fp8, num_blocks, &cv);
+  if (s != MLA_OK) return s;
+  return cache_compact(cv, cache_fp8, block_table, bt_stride, max_pages, seq_lens, node_lens, accept_len, accept_idx,
+                       B, T, new_lens, stream);
+}
+
+// What the page bookkeeping calls share.
+static mla_status check_pages(const int32_t* refs, int num_blocks, const int32_t* block_table, int bt_stride,
+                              int max_pages, int B) {
+  if (B < 0 || num_blocks < 1 || max_pages < 1 || bt_stride < max_pages) return MLA_ERR_ARG;
+  if (max_pages >= (1 << 25) || (long long)B * max_pages >= (1LL << 31)) return MLA_ERR_SHAPE;
+  if (B == 0) return MLA_OK;
+  if (!refs || !block_table) return MLA_ERR_ARG;
+  if (!aligned16(refs) || !aligned16(block_table)) return MLA_ERR_ALIGN;
+  return MLA_OK;
+}
+
+mla_status mla_pages_resize(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
+                            const int32_t* cur_lens, const int32_t* new_lens, int B, int32_t* got_lens,
+                            mla_stream_t stream) {
+  const mla_status s = check_pages(refs, num_blocks, block_table, bt_stride, max_pages, B);
+  if (s != MLA_OK) return s;
+  if (B > 8192) return MLA_ERR_SHAPE;
+  if (B == 0) return MLA_OK;
+  if (!cur_lens || !new_lens || !got_lens) return MLA_ERR_ARG;
+  if (!aligned16(cur_lens) || !aligned16(new_lens) || !aligned16(got_lens)) return MLA_ERR_ALIGN;
+  return cuda_status(launch_pages_resize(refs, num_blocks, block_table, bt_stride, max_pages, cur_lens, new_lens, B,
+                                         got_lens, (cudaStream_t)stream));
+}
+
+mla_status mla_pages_fork(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
+                          int32_t* seq_lens, int B, const int32_t* src, const int32_t* dst, int F, int32_t* copies,
+                          mla_stream_t stream) {
+  const mla_status s = check_pages(refs, num_blocks, block_table, bt_stride, max_pages, B);
+  if (s != MLA_OK) return s;
+  if (F < 0) return MLA_ERR_ARG;
+  if (B > 65536 || F > 4096) return MLA_ERR_SHAPE;
+  if (F == 0) return MLA_OK;
+  if (B == 0 || !seq_lens || !src || !dst || !copies) return MLA_ERR_ARG;
+  if (!aligned16(seq_lens) || !aligned16(src) || !aligned16(dst) || !aligned16(copies)) return MLA_ERR_ALIGN;
+  return cuda_status(launch_pages_fork(refs, num_blocks, block_table, bt_stride, max_pages, seq_lens, B, src, dst, F,
+                                       copies, (cudaStream_t)stream));
+}
+
+static mla_status cache_copy(const CacheView& cv, void* rows_fp8, const int32_t* copies, int n, mla_stream_t stream) {
+  if (n < 0) return MLA_ERR_ARG;
+  if (n == 0) return MLA_OK;
+  if (!copies) return MLA_ERR_ARG;
+  if (!aligned16(copies)) return MLA_ERR_ALIGN;
+  const mla_status s = check_rows32(cv);
+  if (s != MLA_OK) return s;
+  return cuda_status(launch_cache_copy(cv, static_cast<unsigned char*>(rows_fp8), copies, n, (cudaStream_t)stream));
+}
+
+mla_status mla_cache_copy(const mla_cache* cache, const int32_t* copies, int n, mla_stream_t stream) {
+  CacheView cv;
+  const mla_status s = check_cache(cache, &cv);
+  return s != MLA_OK ? s : cache_copy(cv, nullptr, copies, n, stream);
+}
+
+mla_status mla_cache_copy_fp8(void* cache_fp8, int num_blocks, const int32_t* copies, int n, mla_stream_t stream) {
+  CacheView cv;
+  const mla_status s = check_fp8_pool(cache_fp8, num_blocks, &cv);
+  return s != MLA_OK ? s : cache_copy(cv, cache_fp8, copies, n, stream);
 }
 
 mla_status mla_read_device_status(const void* workspace, int* info, mla_stream_t stream) {

@@ -140,6 +140,31 @@ struct AppendCall {
   __nv_bfloat16 *q_nope, *q_pe;
 };
 cudaError_t launch_rope_append(const AppendCall& c, cudaStream_t st);
+// Verification of drafted tokens (mla_verify_tree); probabilities bf16 or fp32.
+constexpr int kMaxTreeNodes = 1024;
+struct VerifyCall {
+  int B, T, V;
+  const void *target, *draft;
+  bool bf16;
+  int64_t row_stride;
+  const int32_t *tokens, *parents, *node_lens;
+  const float *u_accept, *u_sample;
+  int32_t *accept_len, *accept_idx, *out_tokens;
+};
+cudaError_t launch_verify_tree(const VerifyCall& c, cudaStream_t st);
+// Pages: rows_fp8 != null takes the FP8 pool of cv.num_blocks blocks, else cv is the bf16 pool.
+cudaError_t launch_cache_compact(const CacheView& cv, unsigned char* rows_fp8, const int32_t* block_table,
+                                 int bt_stride, int max_pages, const int32_t* seq_lens, const int32_t* node_lens,
+                                 const int32_t* accept_len, const int32_t* accept_idx, int B, int T, int32_t* new_lens,
+                                 cudaStream_t st);
+cudaError_t launch_pages_resize(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
+                                const int32_t* cur_lens, const int32_t* new_lens, int B, int32_t* got_lens,
+                                cudaStream_t st);
+cudaError_t launch_pages_fork(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
+                              int32_t* seq_lens, int B, const int32_t* src, const int32_t* dst, int F,
+                              int32_t* copies, cudaStream_t st);
+cudaError_t launch_cache_copy(const CacheView& cv, unsigned char* rows_fp8, const int32_t* copies, int n,
+                              cudaStream_t st);
 int64_t normal_rows_per_seq(int max_pages);
 cudaError_t launch_normal_expand(const mla_geom* g, const CacheView& cv, const int32_t* block_table, int bt_stride,
                                  const int32_t* seq_lens, int B, int max_pages, const __nv_bfloat16* w_uk,

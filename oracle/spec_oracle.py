@@ -39,3 +39,129 @@ def rope_append_ref(q, kv, q_weight, kv_weight, eps, cos_sin, positions, interle
     q = rms_norm_ref(q, q_weight, eps)
     rows = np.concatenate([rms_norm_ref(kv[:, :512], kv_weight, eps), rotate_ref(kv[:, 512:], cs, interleaved)], -1)
     return q[..., :128], rotate_ref(q[..., 128:], cs[:, None], interleaved), rows
+
+
+# ---------------------------------------------------------------------------
+# Verification of drafted tokens
+# ---------------------------------------------------------------------------
+def verify_ref(target, draft, tokens, parents, n, u_accept, u_sample):
+    """One sequence: (accepted node indices, next token), by rejection sampling with residuals
+    written as normalised distributions: a refused draw x ~ q turns the distribution r into
+    max(r - q, 0) normalised.  target [T, V]; draft [T, V], or None for point masses.
+
+    The rule's first test is against the row as it is (its mass taken as 1).
+    """
+    if n == 0:
+        return [], -1
+    V = target.shape[1]
+    mass = lambda x: np.where(x > 0, x, 0.0)  # noqa: E731  (negative values and NaN are no mass)
+    path, cur = [0], 0
+    left, Z = mass(target[0]), 1.0      # what is left of cur's row, unnormalised, and its mass
+    for t in range(1, n):
+        if parents[t] != cur or not (0 <= tokens[t] < V) or not (0 <= parents[t] < t):
+            continue
+        x = int(tokens[t])
+        q = mass(draft[cur]) if draft is not None else np.eye(1, V, x)[0]
+        if left[x] > 0 and u_accept[t] * q[x] * Z < left[x]:
+            path.append(t)
+            cur, left, Z = t, mass(target[t]), 1.0
+        elif draft is not None:
+            left = np.maximum(left - Z * q, 0.0)
+            Z = float(left.sum())
+        else:
+            Z -= left[x]
+            left = left.copy()
+            left[x] = 0.0
+    if not left.sum() > 0:
+        left = mass(target[cur])
+    if not left.sum() > 0:
+        return path, -1
+    upto = np.cumsum(left)
+    over = np.nonzero(upto > u_sample * upto[-1])[0]
+    return path, int(over[0]) if len(over) else int(np.nonzero(left > 0)[0][-1])
+
+
+# ---------------------------------------------------------------------------
+# Pages
+# ---------------------------------------------------------------------------
+class Pages:
+    """Block table, holders' counts and pool of a paged cache, one page at a time."""
+
+    def __init__(self, block_table, refs, lens, pool=None):
+        self.bt, self.refs, self.lens = block_table.copy(), refs.copy(), lens.copy()
+        self.pool = None if pool is None else pool.copy()
+
+    def _take(self):
+        free = np.nonzero(self.refs == 0)[0]
+        if not len(free):
+            return None
+        self.refs[free[0]] = 1
+        return int(free[0])
+
+    def resize(self, new_lens):
+        held = [(int(s) + 63) // 64 for s in self.lens]
+        for b, s in enumerate(new_lens):
+            for p in range((int(s) + 63) // 64, held[b]):
+                self.refs[self.bt[b, p]] -= 1
+                self.bt[b, p] = -1
+        for b, s in enumerate(new_lens):
+            self.lens[b] = s
+            for p in range(held[b], (int(s) + 63) // 64):
+                k = self._take()
+                if k is None:
+                    self.lens[b] = 64 * p
+                    break
+                self.bt[b, p] = k
+
+    def fork(self, src, dst):
+        """Well-formed forks; returns copies [3, F]."""
+        out = np.zeros((3, len(src)), dtype=np.int32)
+        refs = self.refs.copy()      # who holds what when the call begins
+        for f, (s, d) in enumerate(zip(src, dst)):
+            full, tail = divmod(int(self.lens[s]), 64)
+            out[:, f] = -1, -1, 0
+            if tail and (s != d or refs[self.bt[s, full]] > 1):
+                free = np.nonzero((self.refs == 0) & (refs == 0))[0]
+                if not len(free):
+                    out[0, f] = -2
+                    continue
+                out[:, f] = self.bt[s, full], free[0], tail
+                self.refs[free[0]] = 1
+        for f, (s, d) in enumerate(zip(src, dst)):
+            if out[0, f] == -2:
+                continue
+            full = int(self.lens[s]) // 64
+            if s == d:
+                if out[2, f]:
+                    self.refs[out[0, f]] -= 1
+                    self.bt[d, full] = out[1, f]
+                continue
+            self.bt[d] = -1
+            self.bt[d, :full] = self.bt[s, :full]
+            np.add.at(self.refs, self.bt[s, :full], 1)
+            if out[2, f]:
+                self.bt[d, full] = out[1, f]
+            self.lens[d] = self.lens[s]
+        return out
+
+    def copy(self, copies):
+        for f, t, n in copies.T:
+            if n:
+                self.pool[t, :n] = self.pool[f, :n]
+
+    def compact(self, nodes, accept_len, accept_idx):
+        """The pool after the move, and the new lengths."""
+        was = self.pool.copy()
+        for b in range(len(self.lens)):
+            base = int(self.lens[b] - nodes[b])
+            for i in range(int(accept_len[b])):
+                t, f = base + i, base + int(accept_idx[b, i])
+                self.pool[self.bt[b, t // 64], t % 64] = was[self.bt[b, f // 64], f % 64]
+        return (self.lens - nodes + accept_len).astype(np.int32)
+
+    def check(self):
+        """Every count is the number of table entries that hold the block."""
+        n = np.zeros_like(self.refs)
+        for b, s in enumerate(self.lens):
+            np.add.at(n, self.bt[b, :(int(s) + 63) // 64], 1)
+        assert np.array_equal(n, self.refs)

@@ -56,6 +56,84 @@ def test_rope_append_refusals(mla):
     assert call8(q_pe=None) == mla.MLA_ERR_ARG
 
 
+def test_verify_tree_refusals(mla):
+    names = ["B", "T", "V", "target", "draft", "dtype", "stride", "tokens", "parents", "nodes", "ua", "us", "n", "idx",
+             "out"]
+    ok = dict(B=2, T=4, V=1000, target=0x10000, draft=0x20000, dtype=mla.MLA_DTYPE_F32, stride=1000, tokens=0x30000,
+              parents=0x40000, nodes=None, ua=0x50000, us=0x60000, n=0x70000, idx=0x80000, out=0x90000)
+    call = _caller(mla.mla_verify_tree, names, ok)
+    assert call(B=0) == mla.MLA_OK
+    for kw in (dict(B=-1), dict(T=0), dict(V=0), dict(stride=999), dict(dtype=2), dict(dtype=-1)):
+        assert call(**kw) == mla.MLA_ERR_ARG, kw
+    assert call(T=1025) == mla.MLA_ERR_SHAPE
+    assert call(V=(1 << 30) + 1, stride=1 << 31) == mla.MLA_ERR_SHAPE
+    for name in ("target", "tokens", "parents", "ua", "us", "n", "idx", "out"):
+        assert call(**{name: None}) == mla.MLA_ERR_ARG, name
+    for name in ("target", "draft", "tokens", "parents", "nodes", "ua", "us", "n", "idx", "out"):
+        assert call(**{name: 0x10008}) == mla.MLA_ERR_ALIGN, name
+    assert call(stride=1001) == mla.MLA_ERR_ALIGN
+    assert call(stride=1004, dtype=mla.MLA_DTYPE_BF16) == mla.MLA_ERR_ALIGN     # 2008 bytes
+
+
+def test_cache_compact_and_copy_refusals(mla):
+    names = ["bt", "stride", "mp", "lens", "nodes", "acc", "idx", "B", "T", "new"]
+    ok = dict(bt=0x10000, stride=8, mp=8, lens=0x20000, nodes=0x30000, acc=0x40000, idx=0x50000, B=2, T=4, new=0x60000)
+    for first, bad in ((["cache"], [(dict(cache=_cache(mla, num_blocks=0)), mla.MLA_ERR_ARG),
+                                    (dict(cache=_cache(mla, ckv=0x1004)), mla.MLA_ERR_ALIGN),
+                                    (dict(cache=_cache(mla, num_blocks=1 << 25)), mla.MLA_ERR_SHAPE)]),
+                       (["rows", "nb"], [(dict(rows=None), mla.MLA_ERR_ARG), (dict(nb=0), mla.MLA_ERR_ARG),
+                                         (dict(rows=0x70004), mla.MLA_ERR_ALIGN), (dict(nb=1 << 25), mla.MLA_ERR_SHAPE)])):
+        fp8 = first[0] == "rows"
+        pool = dict(rows=0x70000, nb=8) if fp8 else dict(cache=_cache(mla))
+        call = _caller(mla.mla_cache_compact_fp8 if fp8 else mla.mla_cache_compact, first + names, {**pool, **ok})
+        assert call(B=0) == mla.MLA_OK
+        for kw, want in bad:
+            assert call(**kw) == want, kw
+        for kw in (dict(B=-1), dict(T=0), dict(mp=0), dict(mp=9)):
+            assert call(**kw) == mla.MLA_ERR_ARG, kw
+        assert call(T=1025) == mla.MLA_ERR_SHAPE
+        assert call(mp=1 << 25, stride=1 << 25) == mla.MLA_ERR_SHAPE
+        for name in ("bt", "lens", "acc", "idx", "new"):
+            assert call(**{name: None}) == mla.MLA_ERR_ARG, name
+        for name in ("bt", "lens", "nodes", "acc", "idx", "new"):
+            assert call(**{name: 0x10004}) == mla.MLA_ERR_ALIGN, name
+        for name in ("lens", "nodes", "acc"):     # several CTAs' inputs: the new lengths need their own array
+            assert call(new=ok[name]) == mla.MLA_ERR_ARG, name
+        copy = _caller(mla.mla_cache_copy_fp8 if fp8 else mla.mla_cache_copy, first + ["copies", "n"],
+                       {**pool, "copies": 0x80000, "n": 3})
+        assert copy(n=0) == mla.MLA_OK
+        assert copy(n=-1) == mla.MLA_ERR_ARG
+        assert copy(copies=None) == mla.MLA_ERR_ARG
+        assert copy(copies=0x80008) == mla.MLA_ERR_ALIGN
+        for kw, want in bad:
+            assert copy(**kw) == want, kw
+
+
+def test_pages_resize_and_fork_refusals(mla):
+    names = ["refs", "nb", "bt", "stride", "mp", "cur", "new", "B", "got"]
+    ok = dict(refs=0x10000, nb=64, bt=0x20000, stride=8, mp=8, cur=0x30000, new=0x40000, B=4, got=0x30000)
+    call = _caller(mla.mla_pages_resize, names, ok)
+    assert call(B=0) == mla.MLA_OK
+    for kw in (dict(B=-1), dict(nb=0), dict(mp=0), dict(mp=9), *({n: None} for n in ("refs", "bt", "cur", "new", "got"))):
+        assert call(**kw) == mla.MLA_ERR_ARG, kw
+    for name in ("refs", "bt", "cur", "new", "got"):
+        assert call(**{name: 0x10004}) == mla.MLA_ERR_ALIGN, name
+    assert call(B=8193) == mla.MLA_ERR_SHAPE
+    assert call(mp=1 << 25, stride=1 << 25) == mla.MLA_ERR_SHAPE
+    assert call(B=4096, mp=1 << 20, stride=1 << 20) == mla.MLA_ERR_SHAPE
+
+    names = ["refs", "nb", "bt", "stride", "mp", "lens", "B", "src", "dst", "F", "copies"]
+    call = _caller(mla.mla_pages_fork, names, {**ok, "lens": 0x30000, "src": 0x50000, "dst": 0x60000, "F": 2, "copies": 0x70000})
+    assert call(F=0) == mla.MLA_OK
+    for kw in (dict(B=-1), dict(B=0), dict(F=-1), dict(nb=0), dict(mp=9),
+               *({n: None} for n in ("refs", "bt", "lens", "src", "dst", "copies"))):
+        assert call(**kw) == mla.MLA_ERR_ARG, kw
+    for name in ("refs", "bt", "lens", "src", "dst", "copies"):
+        assert call(**{name: 0x10004}) == mla.MLA_ERR_ALIGN, name
+    assert call(F=4097) == mla.MLA_ERR_SHAPE
+    assert call(B=65537) == mla.MLA_ERR_SHAPE
+
+
 def test_rotation_oracle_is_a_rotation():
     """Inner products of rotated pairs depend on the difference of the angles only, both pairings
     agree up to the order of the values, and position 0 turns nothing."""
