@@ -247,6 +247,37 @@ mla_status mla_decode_sparse(const mla_geom* geom, const mla_batch* batch, const
                              mla_stream_t stream);
 
 /*
+ * Attention of a tree of drafted tokens over the paged cache: the absorbed decode
+ * (Step 3 as in mla_decode) with the tree's visibility in place of the causal one.
+ * Sequence b has S_b = seq_lens[b] cached rows, the last n_b = node_lens[b] of them its
+ * nodes' (node u's row is row S_b - n_b + u; node_lens NULL: n_b = T for all), and query
+ * token t < n_b is node t: it sees the rows j < S_b - n_b, and node u's row where bit
+ * u % 32 of tree_mask[b, t, u / 32] is set (its own among them, if it is to be seen).
+ *   batch: B, T (the most nodes of a sequence, <= 1024), max_pages, num_slots and
+ *     num_splits_override as for mla_decode; causal must be 0.
+ *   node_lens int32 [B], 0 <= n_b <= T; n_b <= S_b unless S_b = 0 (an empty sequence).
+ *   tree_mask uint32 [B, T, ceil(T / 32)]; words of nodes t >= n_b and bits u >= n_b are
+ *     not looked at.
+ *   A query token that sees nothing, and every t >= n_b, gets o_lat = 0 and lse = -inf.
+ *   The rows before the nodes', and each node's row that some node of its sequence
+ *   sees, hold finite values; what other rows hold (NaN too) does not matter.
+ * mla_plan_tree stands in for mla_plan (the same workspace and size), and is re-run
+ * when the lengths or node counts change; the mask is the decode's alone.  checked, the
+ * status word and every other argument as for mla_decode and mla_decode_fp8.
+ */
+mla_status mla_plan_tree(const mla_geom* geom, const mla_batch* batch, const int32_t* seq_lens,
+                         const int32_t* node_lens, void* workspace, size_t ws_bytes, mla_stream_t stream);
+mla_status mla_decode_tree(const mla_geom* geom, const mla_batch* batch, const void* q_lat, const void* q_pe,
+                           const mla_cache* cache, const int32_t* block_table, int bt_stride, const int32_t* seq_lens,
+                           const int32_t* node_lens, const uint32_t* tree_mask, int checked, void* o_lat, float* lse,
+                           void* workspace, size_t ws_bytes, mla_stream_t stream);
+mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, const void* q_lat, const void* q_pe,
+                               const void* cache_fp8, int num_blocks, const int32_t* block_table, int bt_stride,
+                               const int32_t* seq_lens, const int32_t* node_lens, const uint32_t* tree_mask,
+                               int checked, void* o_lat, float* lse, void* workspace, size_t ws_bytes,
+                               mla_stream_t stream);
+
+/*
  * Exact merge of split partial states ("M5.8" 0x0C; "mlxcel" Stage-2
  * contract, here with natural-log LSE):
  * part_o float32 [N, rows, D] (each normalised by its own denominator),

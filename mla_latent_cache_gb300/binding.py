@@ -90,6 +90,9 @@ def _load() -> ctypes.CDLL:
         "mla_normal_chunk_bytes": (ctypes.c_size_t, [G, I, I]),
         "mla_normal_chunk_state_bytes": (ctypes.c_size_t, [G, Bt]),
         "mla_normal_chunked": (I, [G, Bt, P, P, C, P, I, P, P, P, I, P, P, P, P, P]),
+        "mla_plan_tree": (I, [G, Bt, P, P, P, ctypes.c_size_t, P]),
+        "mla_decode_tree": (I, [G, Bt, P, P, C, P, I, P, P, P, I, P, P, P, ctypes.c_size_t, P]),
+        "mla_decode_tree_fp8": (I, [G, Bt, P, P, P, I, P, I, P, P, P, I, P, P, P, ctypes.c_size_t, P]),
         "mla_rope_append": (I, [G, I, P, L64, L64, P, L64, P, P, ctypes.c_float, P, I, P, I, C, P, P, P, P]),
         "mla_rope_append_fp8": (I, [G, I, P, L64, L64, P, L64, P, P, ctypes.c_float, P, I, P, I, P, I, P, P, P, P]),
         "mla_verify_tree": (I, [I, I, I, P, P, I, L64, P, P, P, P, P, P, P, P, P]),
@@ -116,6 +119,7 @@ EXPORTED = ("mla_workspace_size", "mla_plan", "mla_absorb_q", "mla_unabsorb_o", 
             "mla_split_merge", "mla_normal_rows_per_seq", "mla_normal_expanded_bytes", "mla_normal_expand",
             "mla_normal_attention", "mla_normal_chunk_bytes", "mla_normal_chunk_state_bytes", "mla_normal_chunked",
             "mla_rope_append", "mla_rope_append_fp8", "mla_verify_tree",
+            "mla_plan_tree", "mla_decode_tree", "mla_decode_tree_fp8",
             "mla_cache_compact", "mla_cache_compact_fp8", "mla_pages_resize", "mla_pages_fork", "mla_cache_copy",
             "mla_cache_copy_fp8",
             "mla_fp8_pack_cache", "mla_debug_gather", "mla_debug_set_wait_limit", "mla_read_device_status",
@@ -297,6 +301,29 @@ def mla_normal_chunked(geom, batch, q_nope, q_pe, cache: mla_cache, block_table,
                                    ctypes.byref(cache), _ptr(block_table), bt_stride, _ptr(seq_lens), _ptr(w_uk),
                                    _ptr(w_uv), int(chunk_rows), _ptr(kv_chunk), _ptr(state), _ptr(o), _ptr(lse),
                                    _stream(stream))
+
+
+def mla_plan_tree(geom, batch, seq_lens, node_lens, workspace, ws_bytes: int, stream=None) -> int:
+    """The plan of a tree decode (node_lens None: T nodes each)."""
+    return _lib.mla_plan_tree(ctypes.byref(geom), ctypes.byref(batch), _ptr(seq_lens), _ptr(node_lens),
+                              _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def mla_decode_tree(geom, batch, q_lat, q_pe, cache: mla_cache, block_table, bt_stride: int, seq_lens, node_lens,
+                    tree_mask, checked: int, o_lat, lse, workspace, ws_bytes: int, stream=None) -> int:
+    """Attention of a tree of drafted tokens (bit words tree_mask [B, T, ceil(T/32)]) over the cache."""
+    return _lib.mla_decode_tree(ctypes.byref(geom), ctypes.byref(batch), _ptr(q_lat), _ptr(q_pe), ctypes.byref(cache),
+                                _ptr(block_table), bt_stride, _ptr(seq_lens), _ptr(node_lens), _ptr(tree_mask),
+                                int(checked), _ptr(o_lat), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def mla_decode_tree_fp8(geom, batch, q_lat, q_pe, cache_fp8, num_blocks: int, block_table, bt_stride: int, seq_lens,
+                        node_lens, tree_mask, checked: int, o_lat, lse, workspace, ws_bytes: int, stream=None) -> int:
+    """The same over FP8 rows (uint8 [num_blocks, 64, 656])."""
+    return _lib.mla_decode_tree_fp8(ctypes.byref(geom), ctypes.byref(batch), _ptr(q_lat), _ptr(q_pe), _ptr(cache_fp8),
+                                    int(num_blocks), _ptr(block_table), bt_stride, _ptr(seq_lens), _ptr(node_lens),
+                                    _ptr(tree_mask), int(checked), _ptr(o_lat), _ptr(lse), _ptr(workspace), ws_bytes,
+                                    _stream(stream))
 
 
 def mla_rope_append(geom, N: int, q, q_token_stride: int, q_head_stride: int, kv, kv_token_stride: int, q_weight,

@@ -62,6 +62,15 @@
 // decode's listed rows (copied by whole warps with cp.async); FP8 656-byte
 // rows, converted to bf16 in shared memory by four more warps (512 threads).
 //
+// Trees of drafted tokens (template kTree, pages through the block table): the
+// last n_b cache rows of a sequence are its nodes' rows, and node t sees the rows
+// before them and those of its bit words.  Only the pages that reach into the
+// nodes' rows (one to three of a sequence) differ: a softmax thread then takes the
+// sixteen visibility bits of its columns, which it asks for before it waits for the
+// page's scores, and rows that no node of the group sees are zeroed in shared memory
+// like those past the sequence end, so that what they hold never reaches the
+// accumulator (0 * NaN).  The rate is the causal decode's at equal rows.
+//
 // Every wait is bounded; a wait that runs out records MLA_ERR_TIMEOUT in the
 // workspace and raises a CTA-wide abort flag.  Loads and MMAs already issued
 // are drained, and both CTAs meet at a final cluster barrier before the
@@ -196,6 +205,9 @@ struct FastArgs {
   long long ckv_row, kpe_row;
   int kpe_separate;          // RoPE values not at latent + 512 in the same rows: loaded by their own box
   float scale_log2;          // softmax scale times log2(e)
+  const int32_t* node_lens;  // trees: nodes of each sequence (null: T)
+  const uint32_t* tree_mask; // trees: [B, T, tree_words], bit u of node t's words: t sees node u
+  int tree_words;
   __nv_bfloat16* o_lat;
   float* lse;
   WsLayout L;
@@ -273,8 +285,12 @@ __device__ __forceinline__ uint64_t vdesc(uint32_t saddr) { return sw128_desc(sa
 struct SegRows {
   int b, p0, p1, slot_out, merge_rec, S, fr, limit;
   bool row_valid;
+  // Trees: limit is the row's count of leading rows that it sees in any case (0: it
+  // sees nothing, a node past the sequence's count), nodes the sequence's node count.
+  int rb, nodes;
 };
 
+template <bool kTree>
 __device__ __forceinline__ SegRows seg_rows(const int* rec, const FastArgs& a, int R, int row) {
   SegRows s;
   s.b = rec[0];
@@ -286,8 +302,37 @@ __device__ __forceinline__ SegRows seg_rows(const int* rec, const FastArgs& a, i
   s.S = S < 0 ? 0 : min(S, a.max_rows);
   s.fr = rec[1] * kRowsPerBlock + row;
   s.row_valid = s.fr < R;
-  s.limit = s.row_valid ? visible_limit(s.S, a.T, s.fr / a.H, a.causal) : 0;
+  if constexpr (kTree) {
+    s.rb = rec[1];
+    s.nodes = tree_nodes(a.node_lens, s.b, a.T, s.S);
+    s.limit = s.row_valid && s.fr / a.H < s.nodes ? s.S - s.nodes : -1;
+  } else {
+    s.limit = s.row_valid ? visible_limit(s.S, a.T, s.fr / a.H, a.causal) : 0;
+  }
   return s;
+}
+
+// Trees: the visibility bits of cache rows j0 .. j0 + 15 for the row's node.
+__device__ __forceinline__ uint32_t tree_bits(const FastArgs& a, const SegRows& s, int j0) {
+  if (s.limit < 0) return 0;
+  const int u0 = j0 - s.limit;               // node of the first of them; negative: a row before the nodes
+  const int count = s.nodes - u0;            // how many there are before the sequence end
+  if (count <= 0) return 0;
+  const uint32_t* m = a.tree_mask + ((size_t)s.b * a.T + s.fr / a.H) * a.tree_words;
+  const int w = u0 >> 5;                     // -1 for a negative u0 (u0 >= -15 where this is called)
+  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : __ldg(m + w);
+  const uint32_t hi = w + 1 < a.tree_words ? __ldg(m + w + 1) : 0u;
+  const uint32_t bits = __funnelshift_r(lo, hi, u0 & 31);
+  return count < 16 ? bits & ((1u << count) - 1u) : bits & 0xFFFFu;
+}
+// Trees: whether any node of the segment's query-row group sees node u (0 <= u < nodes).
+__device__ __forceinline__ bool tree_seen(const FastArgs& a, const SegRows& s, int u) {
+  const int t0 = s.rb * kRowsPerBlock / a.H;
+  const int t1 = min(s.nodes, t0 + (kRowsPerBlock + a.H - 1) / a.H);
+  const uint32_t* m = a.tree_mask + ((size_t)s.b * a.T + t0) * a.tree_words + (u >> 5);
+  uint32_t any = 0;
+  for (int t = t0; t < t1; ++t, m += a.tree_words) any |= __ldg(m);
+  return (any >> (u & 31)) & 1u;
 }
 
 // Block id `blk` of page p of sequence b (read from the table by the caller)
@@ -871,7 +916,8 @@ __device__ __forceinline__ void reload_role(const Shared& sh, const CUtensorMap*
 // (tm_aux) bytes wide, 32 rows high, and tm_kpe the rows' RoPE values as bf16
 // (64 x 32 boxes, 128-byte swizzled); tm_page unused.  tm_aux is unused by the
 // other modes.
-template <int kMode>
+// kTree: trees of drafted tokens (see the file's head; pages through the block table).
+template <int kMode, bool kTree>
 __global__ void __launch_bounds__(threads_of<kMode>(), 1)
     decode_sm103_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qpe,
                         const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_pair,
@@ -974,12 +1020,13 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
 
   if (a.checked && blockIdx.x == 0 && tid == 0) {
     if (hdr[MLA_HDR_MAGIC] != MLA_PLAN_MAGIC || hdr[MLA_HDR_B] != a.B || hdr[MLA_HDR_T] != a.T ||
-        hdr[MLA_HDR_H] != a.H || hdr[MLA_HDR_CAUSAL] != a.causal) {
+        hdr[MLA_HDR_H] != a.H || hdr[MLA_HDR_CAUSAL] != (kTree ? kPlanTree : a.causal)) {
       record_error(hdr, MLA_ERR_PLAN_STALE, 0);
     } else {
       unsigned h = 0;
       for (int b = 0; b < a.B; ++b) {
         unsigned S = (unsigned)a.seq_lens[b / a.seq_div];
+        if constexpr (kTree) S += kNodeStamp * (unsigned)(a.node_lens ? a.node_lens[b] : a.T);
         unsigned x = (unsigned)b + 0x632BE5ABu;
         x ^= x >> 16; x *= 0x7feb352dU; x ^= x >> 15; x *= 0x846ca68bU; x ^= x >> 16;
         unsigned y = S * 0x9E3779B1u + x;
@@ -1178,7 +1225,7 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
     bool ok = true;
     SegRows cur;
     if (si >= 0) {
-      cur = seg_rows(seg + (size_t)si * kSegWords, a, R, row);
+      cur = seg_rows<kTree>(seg + (size_t)si * kSegWords, a, R, row);
       if (!stage_q(cur, 0)) { fail(hdr, abort_flag, 33); ok = false; }
     }
     while (ok && si >= 0) {
@@ -1188,6 +1235,10 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
         const int sb = g & 1, st = g % kStages, pb = g % kPBufs;
         const int page = cur.p0 + i;
         const int jbase = page * kPage + kHalfRows * kh + 16 * cw;   // first cache row of this thread's columns
+        uint32_t vis = 0xFFFFu;   // trees: the visible columns of a page that is not seen as a whole
+        if constexpr (kTree) {
+          if (jbase + 16 > cur.limit) vis = tree_bits(a, cur, jbase);
+        }
         bool w_ok = mbar_wait(sh.bar(BAR_S_FULL + sb), (g >> 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, w_ok)) { fail(hdr, abort_flag, 30); ok = false; break; }
         tc_fence_after();
@@ -1207,7 +1258,7 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (jbase + j < cur.limit) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sr[j]));
+            if (kTree ? (vis >> j) & 1u : jbase + j < cur.limit) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sr[j]));
         }
         float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         {
@@ -1245,7 +1296,7 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
         for (int j = 0; j < 16; ++j) x[j] = ex2(fmaf(__uint_as_float(sr[j]), a.scale_log2, -m_use));
         if (!full) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = (jbase + j < cur.limit) ? x[j] : 0.f;
+          for (int j = 0; j < 16; ++j) x[j] = (kTree ? (vis >> j) & 1u : jbase + j < cur.limit) ? x[j] : 0.f;
         }
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pw[8];
@@ -1275,14 +1326,19 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
         }
         // Rows of the last page past the sequence end are zeroed in the eight latent
         // slots P V reads, once the other half's rows (reloaded after Q K^T) landed.
+        // (Trees: and those of nodes that no node of this group sees.)
         const int valid = cur.S - page * kPage;
-        if (valid < kPage) {
+        const int prefix = kTree ? valid - cur.nodes : valid;   // rows of the page before the nodes'
+        if ((kTree ? prefix : valid) < kPage) {
           w_ok = mbar_wait(sh.bar(BAR_RELOAD + st), (g / kStages) & 1, abort_flag);
           if (!__all_sync(0xffffffffu, w_ok)) { fail(hdr, abort_flag, 35); ok = false; break; }
           // After the reload, latent slot s holds rows of page half (s >> 1) & 1 in both CTAs.
           const int idx = tid - 128;   // 0..255: slot idx / 32, row idx % 32
           const int s_ = idx / kHalfRows, rr = idx % kHalfRows;
-          if (((s_ >> 1) & 1) * kHalfRows + rr >= valid) {
+          const int pr = ((s_ >> 1) & 1) * kHalfRows + rr;
+          bool out = pr >= valid;
+          if constexpr (kTree) out = out || (pr >= prefix && !tree_seen(a, cur, pr - prefix));
+          if (out) {
             const uint32_t dst = sh.slot(st, s_) + rr * 128;
 #pragma unroll
             for (int z = 0; z < 8; ++z)
@@ -1299,7 +1355,7 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
       const int si_next = walk.cur();
       SegRows nxt = cur;
       if (si_next >= 0) {
-        nxt = seg_rows(seg + (size_t)si_next * kSegWords, a, R, row);
+        nxt = seg_rows<kTree>(seg + (size_t)si_next * kSegWords, a, R, row);
         if (!stage_q(nxt, sc + 1)) { fail(hdr, abort_flag, 33); ok = false; break; }
       }
       // Epilogue: wait for the last P V, combine the four quarters of the row sum,
@@ -1533,12 +1589,12 @@ bool set_kernel_attributes() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(decode_sm103_kernel<kModeDense>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemAlloc) != cudaSuccess ||
-        cudaFuncSetAttribute(decode_sm103_kernel<kModeSparse>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemAlloc) != cudaSuccess ||
-        cudaFuncSetAttribute(decode_sm103_kernel<kModeFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemAlloc) != cudaSuccess)
+    auto allow = [](auto kernel) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc) == cudaSuccess;
+    };
+    if (!allow(decode_sm103_kernel<kModeDense, false>) || !allow(decode_sm103_kernel<kModeSparse, false>) ||
+        !allow(decode_sm103_kernel<kModeFp8, false>) || !allow(decode_sm103_kernel<kModeDense, true>) ||
+        !allow(decode_sm103_kernel<kModeFp8, true>))
       return false;
     done[dev].store(true, std::memory_order_release);
   }
@@ -1579,7 +1635,7 @@ int decode_sm103_pairs_per_device() {
       cudaLaunchConfig_t cfg;
       cudaLaunchAttribute attr[2];
       cluster_launch_config(&cfg, attr, 256, 0, false);
-      if (cudaOccupancyMaxActiveClusters(&n, decode_sm103_kernel<kModeDense>, &cfg) != cudaSuccess) n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, decode_sm103_kernel<kModeDense, false>, &cfg) != cudaSuccess) n = 0;
     }
     if (n <= 0) {
       const int sms = mla_device_sm_count();
@@ -1595,7 +1651,7 @@ cudaError_t launch_decode_sm103(const mla_geom* g, const mla_batch* b, const WsL
                                 const __nv_bfloat16* q_lat, const __nv_bfloat16* q_pe, const CacheView& cv,
                                 const int32_t* block_table, int bt_stride, const int32_t* seq_lens, int checked,
                                 __nv_bfloat16* o_lat, float* lse, void* ws, cudaStream_t st, const SparseList* sparse,
-                                const Fp8Pool* fp8) {
+                                const Fp8Pool* fp8, const TreeNodes* tree) {
   const long long rows_total = (long long)b->B * b->T * g->H;
   CUtensorMap m_qlat, m_qpe, m_page, m_pair, m_kpe, m_aux;
   {
@@ -1644,6 +1700,9 @@ cudaError_t launch_decode_sm103(const mla_geom* g, const mla_batch* b, const WsL
   a.kpe_separate = combined ? 0 : 1;
   a.ckv = cv.ckv; a.kpe = cv.kpe; a.ckv_row = cv.ckv_row; a.kpe_row = cv.kpe_row;
   a.scale_log2 = g->softmax_scale * 1.4426950408889634f;
+  a.node_lens = tree ? tree->node_lens : nullptr;
+  a.tree_mask = tree ? tree->mask : nullptr;
+  a.tree_words = tree ? (b->T + 31) / 32 : 0;
   a.o_lat = o_lat; a.lse = lse; a.L = L;
   if (!set_kernel_attributes()) return cudaErrorInvalidValue;
   int pairs = L.cap_ranges;
@@ -1654,12 +1713,13 @@ cudaError_t launch_decode_sm103(const mla_geom* g, const mla_batch* b, const WsL
   cudaLaunchAttribute attr[2];
   cluster_launch_config(&cfg, attr, pairs, st, true, fp8 ? kFp8Threads : kThreads);
   char* w = reinterpret_cast<char*>(ws);
-  if (fp8)
-    return cudaLaunchKernelEx(&cfg, decode_sm103_kernel<kModeFp8>, m_qlat, m_qpe, m_page, m_pair, m_kpe, m_aux, a, w);
-  if (sparse)
-    return cudaLaunchKernelEx(&cfg, decode_sm103_kernel<kModeSparse>, m_qlat, m_qpe, m_page, m_pair, m_kpe, m_aux, a,
-                              w);
-  return cudaLaunchKernelEx(&cfg, decode_sm103_kernel<kModeDense>, m_qlat, m_qpe, m_page, m_pair, m_kpe, m_aux, a, w);
+  auto launch = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, m_qlat, m_qpe, m_page, m_pair, m_kpe, m_aux, a, w);
+  };
+  if (tree) return fp8 ? launch(decode_sm103_kernel<kModeFp8, true>) : launch(decode_sm103_kernel<kModeDense, true>);
+  if (fp8) return launch(decode_sm103_kernel<kModeFp8, false>);
+  if (sparse) return launch(decode_sm103_kernel<kModeSparse, false>);
+  return launch(decode_sm103_kernel<kModeDense, false>);
 }
 
 cudaError_t set_pipeline_wait_limit(long long cycles) {

@@ -94,9 +94,25 @@ __host__ __device__ __forceinline__ int visible_limit(int S, int T, int t, int c
   return v < 0 ? 0 : (v > S ? S : v);
 }
 
+// Trees of drafted tokens: the last n_b cache rows of sequence b are its nodes', n_b =
+// node_lens[b] (null: T), as far as it has rows at all.
+__host__ __device__ __forceinline__ int tree_nodes(const int32_t* node_lens, int b, int T, int S) {
+  int n = node_lens ? node_lens[b] : T;
+  n = n < T ? n : T;
+  n = n < S ? n : S;
+  return n < 0 ? 0 : n;
+}
+struct TreeNodes {
+  const int32_t* node_lens;
+  const uint32_t* mask;      // [B, T, ceil(T / 32)]; the planner does not read it
+};
+constexpr int kPlanTree = 2;                    // a tree plan's MLA_HDR_CAUSAL
+constexpr unsigned kNodeStamp = 0x85EBCA6Bu;    // a sequence's stamp: length + kNodeStamp * nodes
+
 // Launchers (one per translation unit); all return cudaError_t of the launch.
 cudaError_t launch_plan(const int32_t* seq_lens, const mla_geom* g, const mla_batch* b,
-                        const WsLayout& L, void* ws, cudaStream_t st, int seq_div = 1, int max_rows = 0);
+                        const WsLayout& L, void* ws, cudaStream_t st, int seq_div = 1, int max_rows = 0,
+                        const TreeNodes* tree = nullptr);
 // The sparse decode's index lists: physical rows indices [B', topk] for the
 // B' = B * seq_div (sequence, query token) pairs, lengths seq_lens[b' / seq_div].
 struct SparseList {
@@ -112,7 +128,8 @@ cudaError_t launch_decode_sm103(const mla_geom* g, const mla_batch* b, const WsL
                                 const __nv_bfloat16* q_lat, const __nv_bfloat16* q_pe, const CacheView& cv,
                                 const int32_t* block_table, int bt_stride, const int32_t* seq_lens, int checked,
                                 __nv_bfloat16* o_lat, float* lse, void* ws, cudaStream_t st,
-                                const SparseList* sparse = nullptr, const Fp8Pool* fp8 = nullptr);
+                                const SparseList* sparse = nullptr, const Fp8Pool* fp8 = nullptr,
+                                const TreeNodes* tree = nullptr);
 int decode_sm103_pairs_per_device();
 cudaError_t launch_split_merge(const float* part_o, const float* part_lse, const int32_t* indptr, int M,
                                int rows, int D, __nv_bfloat16* o, float* lse, cudaStream_t st);

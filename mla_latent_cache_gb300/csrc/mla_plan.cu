@@ -99,6 +99,8 @@ struct PlanArgs {
   int B, T, H, causal, G, N, max_pages;
   int max_rows;              // longest allowed length: max_pages * 64, or the sparse decode's topk
   int RB, num_groups;
+  int tree;                  // trees of drafted tokens: sequence b has node_lens[b] query tokens (null: T)
+  const int32_t* node_lens;
   WsLayout L;
 };
 
@@ -159,8 +161,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
   int errb = INT_MAX;
   for (int b = tid; b < a.B; b += blockDim.x) {
     const int S = a.seq_lens[b / a.seq_div];
-    hsum += mix32((uint32_t)S * 0x9E3779B1u + mix32((uint32_t)b + 0x632BE5ABu));
-    if (S < 0 || S > a.max_rows || (S > 0 && S < a.T)) errb = min(errb, b);
+    // query tokens of the sequence: T, or its tree's nodes (a count outside [0, T] is reported)
+    const int n = a.tree && a.node_lens ? a.node_lens[b] : a.T;
+    const uint32_t stamp = (uint32_t)S + (a.tree ? kNodeStamp * (uint32_t)n : 0u);
+    hsum += mix32(stamp * 0x9E3779B1u + mix32((uint32_t)b + 0x632BE5ABu));
+    if (S < 0 || S > a.max_rows || (S > 0 && S < n) || n < 0 || n > a.T) errb = min(errb, b);
   }
 
   // Pass A: pages per group and their exclusive prefix.
@@ -174,7 +179,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
       int S = a.seq_lens[b / a.seq_div];
       S = S < 0 ? 0 : (S > a.max_rows ? a.max_rows : S);
       const int r_last = min(R, (rb + 1) * kRowsPerBlock) - 1;
-      const int vis = visible_limit(S, a.T, r_last / a.H, a.causal);
+      int vis = visible_limit(S, a.T, r_last / a.H, a.causal);
+      // a group of rows past a tree's nodes needs no page
+      if (a.tree && rb * kRowsPerBlock / a.H >= tree_nodes(a.node_lens, b, a.T, S)) vis = 0;
       n = (vis + kPage - 1) / kPage;
     }
     int v[3] = {n, n > 0 ? 1 : 0, 0}, tot[3];
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
   for (int r = num_ranges + 1 + tid; r <= a.L.cap_ranges; r += blockDim.x) rptr[r] = total_seg;
   if (tid == 0) {
     rptr[num_ranges] = total_seg;
-    hdr[MLA_HDR_B] = a.B; hdr[MLA_HDR_T] = a.T; hdr[MLA_HDR_H] = a.H; hdr[MLA_HDR_CAUSAL] = a.causal;
+    hdr[MLA_HDR_B] = a.B; hdr[MLA_HDR_T] = a.T; hdr[MLA_HDR_H] = a.H; hdr[MLA_HDR_CAUSAL] = a.tree ? kPlanTree : a.causal;
     hdr[MLA_HDR_NUM_GROUPS] = a.num_groups;
     hdr[MLA_HDR_NUM_SEGMENTS] = total_seg;
     hdr[MLA_HDR_NUM_RANGES] = num_ranges;
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
 }  // namespace
 
 cudaError_t launch_plan(const int32_t* seq_lens, const mla_geom* g, const mla_batch* b, const WsLayout& L,
-                        void* ws, cudaStream_t st, int seq_div, int max_rows) {
+                        void* ws, cudaStream_t st, int seq_div, int max_rows, const TreeNodes* tree) {
   PlanArgs a;
   a.seq_lens = seq_lens;
   a.seq_div = seq_div;
@@ -317,6 +324,8 @@ cudaError_t launch_plan(const int32_t* seq_lens, const mla_geom* g, const mla_ba
   a.max_rows = max_rows > 0 ? max_rows : b->max_pages * kPage;
   a.RB = (b->T * g->H + kRowsPerBlock - 1) / kRowsPerBlock;
   a.num_groups = b->B * a.RB;
+  a.tree = tree != nullptr;
+  a.node_lens = tree ? tree->node_lens : nullptr;
   a.L = L;
   return launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, reinterpret_cast<char*>(ws));
 }

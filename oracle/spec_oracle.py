@@ -165,3 +165,63 @@ class Pages:
         for b, s in enumerate(self.lens):
             np.add.at(n, self.bt[b, :(int(s) + 63) // 64], 1)
         assert np.array_equal(n, self.refs)
+
+
+# ---------------------------------------------------------------------------
+# Attention of a tree of drafted tokens
+# ---------------------------------------------------------------------------
+def tree_visible(S: int, n: int, see: np.ndarray) -> np.ndarray:
+    """Boolean [T, S]: node t < n sees the rows before the last n, and row S - n + u where see[t, u]."""
+    T = see.shape[0]
+    m = np.zeros((T, S), dtype=bool)
+    m[:n, :S - n] = True
+    m[:n, S - n:] = see[:n, :n]
+    return m
+
+
+def tree_decode_ref(q_lat, q_pe, pool, block_table, seq_lens, node_lens, see, scale=1.0 / np.sqrt(192.0)):
+    """(o_lat [B,T,H,512], lse [B,T,H]); pool [num_blocks, 64, 576], see boolean [B, T, T].
+
+    Only the rows that a node sees take part in its sums.
+    """
+    B, T, H, _ = q_lat.shape
+    o = np.zeros((B, T, H, 512))
+    lse = np.full((B, T, H), -np.inf)
+    for b in range(B):
+        S, n = int(seq_lens[b]), min(int(node_lens[b]), int(seq_lens[b]))
+        if S == 0:
+            continue
+        rows = pool[block_table[b, :(S + 63) // 64]].reshape(-1, 576)[:S]
+        vis = tree_visible(S, n, see[b])
+        for t in range(n):
+            r = rows[vis[t]]
+            if not len(r):
+                continue
+            x = (q_lat[b, t] @ r[:, :512].T + q_pe[b, t] @ r[:, 512:].T) * scale
+            m = x.max(-1, keepdims=True)
+            p = np.exp(x - m)
+            lse[b, t] = (m + np.log(p.sum(-1, keepdims=True)))[:, 0]
+            o[b, t] = p @ r[:, :512] / p.sum(-1, keepdims=True)
+    return o, lse
+
+
+def see_words(see: np.ndarray) -> np.ndarray:
+    """Boolean [B, T, T] as bit words int32 [B, T, ceil(T / 32)]; spare bits are set (nobody may look at them)."""
+    B, T, _ = see.shape
+    W = (T + 31) // 32
+    bits = np.ones((B, T, 32 * W), dtype=np.uint64)
+    bits[..., :T] = see
+    return (bits.reshape(B, T, W, 32) << np.arange(32, dtype=np.uint64)).sum(-1).astype(np.uint32).view(np.int32)
+
+
+def ancestors(parents: np.ndarray) -> np.ndarray:
+    """Boolean [B, T, T]: node t sees itself and the nodes above it; parents[b, t] < t."""
+    B, T = parents.shape
+    see = np.zeros((B, T, T), dtype=bool)
+    for b in range(B):
+        for t in range(T):
+            u = t
+            while u >= 0:
+                see[b, t, u] = True
+                u = int(parents[b, u]) if u else -1
+    return see

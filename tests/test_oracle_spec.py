@@ -113,3 +113,49 @@ def test_pages_hold_what_the_table_says():
         g.resize(n)
         g.fork([s], [d])
         g.check()
+
+
+def test_tree_decode_reduces_to_the_causal_one():
+    """A chain's tree attention is the causal decode of the T new rows, which is pinned on its own;
+    a full mask is the non-causal one; a tree of one node is a decode step of one token."""
+    from oracle import mla_oracle as M
+    rng = np.random.default_rng(0)
+    B, T, H = 3, 5, 2
+    lens = np.array([70, 5, 130])
+    bt = rng.permutation(8)[:6].reshape(3, 2)
+    bt = np.concatenate([bt, [[6], [6], [7]]], 1)
+    pool = rng.standard_normal((8, 64, 576))
+    ql, qp = rng.standard_normal((B, T, H, 512)) * 0.3, rng.standard_normal((B, T, H, 64))
+    chain = O.ancestors(np.tile(np.arange(-1, T - 1), (B, 1)))
+    assert np.array_equal(chain[0], np.tril(np.ones((T, T), dtype=bool)))
+    for see, causal in ((chain, True), (np.ones((B, T, T), dtype=bool), False)):
+        o, l = O.tree_decode_ref(ql, qp, pool, bt, lens, [T] * B, see)
+        ro, rl = M.decode_ref(ql, qp, pool, bt, lens, causal)
+        assert np.allclose(o, ro, atol=1e-12) and np.allclose(l, rl, atol=1e-12)
+
+
+def test_tree_decode_is_its_branches_decoded_alone():
+    """Each branch, as a chain over the prefix and its own rows only, gives the same last row."""
+    from oracle import mla_oracle as M
+    rng = np.random.default_rng(1)
+    S, T, H = 80, 6, 2
+    parents = np.array([[-1, 0, 0, 1, 2, 2]])
+    see = O.ancestors(parents)
+    pool = rng.standard_normal((2, 64, 576))
+    ql, qp = rng.standard_normal((1, T, H, 512)) * 0.3, rng.standard_normal((1, T, H, 64))
+    o, l = O.tree_decode_ref(ql, qp, pool, np.array([[0, 1]]), [S], [T], see)
+    flat = pool.reshape(-1, 576)
+    for t in range(T):
+        rows = np.concatenate([flat[:S - T], flat[S - T:S][see[0, t]]])
+        alone = np.zeros((2, 64, 576))
+        alone.reshape(-1, 576)[:len(rows)] = rows
+        ro, rl = M.decode_ref(ql[:, t:t + 1], qp[:, t:t + 1], alone, np.array([[0, 1]]), np.array([len(rows)]), False)
+        assert np.allclose(o[0, t], ro[0, 0], atol=1e-12) and np.allclose(l[0, t], rl[0, 0], atol=1e-12)
+
+
+def test_see_words():
+    see = np.zeros((1, 34, 34), dtype=bool)
+    see[0, 1, [0, 31, 32]] = True
+    w = O.see_words(see).view(np.uint32)
+    assert w.shape == (1, 34, 2)
+    assert w[0, 1].tolist() == [0x80000001, 0xFFFFFFFD] and w[0, 0].tolist() == [0, 0xFFFFFFFC]

@@ -134,6 +134,42 @@ def test_pages_resize_and_fork_refusals(mla):
     assert call(B=65537) == mla.MLA_ERR_SHAPE
 
 
+def test_tree_decode_refusals(mla):
+    g, b = mla.make_geom(16), mla.make_batch(2, 8, False, 8, num_slots=4)
+    ws = mla.mla_workspace_size(g, b)
+    plan = _caller(mla.mla_plan_tree, ["geom", "batch", "lens", "nodes", "ws", "bytes"],
+                   dict(geom=g, batch=b, lens=0x10000, nodes=0x20000, ws=0x40000, bytes=ws))
+    names = ["geom", "batch", "q_lat", "q_pe", "cache", "bt", "stride", "lens", "nodes", "mask", "checked", "o", "lse",
+             "ws", "bytes"]
+    ok = dict(geom=g, batch=b, q_lat=0x10000, q_pe=0x20000, cache=_cache(mla), bt=0x30000, stride=8, lens=0x40000,
+              nodes=0x50000, mask=0x60000, checked=0, o=0x70000, lse=0x80000, ws=0x90000, bytes=ws)
+    dec = _caller(mla.mla_decode_tree, names, ok)
+    names8 = names[:4] + ["rows", "nb"] + names[5:]
+    dec8 = _caller(mla.mla_decode_tree_fp8, names8, {**ok, "rows": 0xA0000, "nb": 8})
+    for call in (plan, dec, dec8):
+        assert call(batch=mla.make_batch(2, 8, True, 8, num_slots=4)) == mla.MLA_ERR_ARG      # causal
+        assert call(batch=mla.make_batch(2, 0, False, 8, num_slots=4)) == mla.MLA_ERR_ARG
+        assert call(batch=mla.make_batch(2, 1025, False, 8, num_slots=4)) == mla.MLA_ERR_SHAPE
+        assert call(geom=mla.make_geom(24)) == mla.MLA_ERR_SHAPE
+        assert call(bytes=ws - 1) == mla.MLA_ERR_WORKSPACE
+        assert call(ws=None) == mla.MLA_ERR_ARG
+        assert call(ws=0x90010) == mla.MLA_ERR_ALIGN
+        assert call(lens=None) == mla.MLA_ERR_ARG
+        for name in ("lens", "nodes"):
+            assert call(**{name: 0x10004}) == mla.MLA_ERR_ALIGN, name
+    for call in (dec, dec8):
+        assert call(batch=mla.make_batch(0, 8, False, 8, num_slots=4)) == mla.MLA_OK
+        for name in ("q_lat", "q_pe", "bt", "mask", "o", "lse"):
+            assert call(**{name: None}) == mla.MLA_ERR_ARG, name
+            assert call(**{name: 0x10004}) == mla.MLA_ERR_ALIGN, name
+        assert call(o=0x70010) == mla.MLA_ERR_ALIGN
+        assert call(stride=7) == mla.MLA_ERR_ARG
+    assert dec(cache=_cache(mla, num_blocks=0)) == mla.MLA_ERR_ARG
+    assert dec8(rows=None) == mla.MLA_ERR_ARG
+    assert dec8(nb=0) == mla.MLA_ERR_ARG
+    assert dec8(rows=0xA0008) == mla.MLA_ERR_ALIGN
+
+
 def test_rotation_oracle_is_a_rotation():
     """Inner products of rotated pairs depend on the difference of the angles only, both pairings
     agree up to the order of the values, and position 0 turns nothing."""
