@@ -477,7 +477,7 @@ mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64
  *     probabilities of the token after node t, and those that node t's children were
  *     drawn from (independent draws; not read at nodes without children).  draft_probs
  *     NULL: each draft is taken as certain (a point mass), as the likeliest tokens of a
- *     drafter are.  Negative values and NaN count as 0; rows need not sum to 1 exactly.
+ *     drafter are.  Negative values, infinities and NaN count as 0; rows need not sum to 1 exactly.
  *   u_accept float32 [B, T] (node t's number), u_sample float32 [B]: in [0, 1).
  * Rule: from cur = 0, the children of cur are tried in index order.  With p, q the rows
  * of cur, k of its children refused so far, R_k = max(p - C_k q, 0), C_0 = 0, Z_0 = 1,

@@ -142,10 +142,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _torch_stream() -> int:
+    """The handle of torch's current stream (of the current device)."""
+    global _torch_stream
+    import torch
+    torch.cuda.init()
+    device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    # (torch.cuda.current_stream().cuda_stream without the Stream object: 0.2 us instead of 3)
+    _torch_stream = lambda: raw(device())  # noqa: E731
+    return _torch_stream()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _torch_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -16,15 +16,30 @@
 // refused here, Z_k = 1 - their probabilities, and x is accepted when u Z_k < R_k(x).
 //
 // The draw: the first x, in vocabulary order, with R(0) + ... + R(x) > u_sample * Z.
-// Decisions lie next to borders, so every product and sum is fp64 (the inputs are fp32
-// or bf16, so u q(x) and the widened values are exact).
+//
+// Decisions lie next to borders, so sums are kept to about 1e-13 of the mass: the
+// inputs are fp32 or bf16 (u q(x) and the widened values are exact in fp64), the walk's
+// scalars are fp64, and a row is summed by each lane in pairs of fp32 (a value and what
+// its rounding lost; every difference p - C q and every addition keeps its error term),
+// joined in fp64.  The fp64 pipe does two operations per cycle and SM here: a row of
+// fp64 additions took 286 us for 64 sequences of 129280 entries, where reading takes 10.
+//
+// Bound by memory: of T rows only those at which a draft is refused are read, p and q
+// once each, and once more the sixteenth of a slice that holds the drawn token.  A
+// cluster of CTAs shares a sequence (each a contiguous slice of the vocabulary), since
+// one CTA alone reads ~0.1 TB/s; masses are exchanged through distributed shared
+// memory.  Every CTA walks the tree alike (one warp, from shared memory).
+#include <math.h>
+
 #include "mla_internal.cuh"
+#include "sm103_ptx.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr int kTile = 256;          // vocabulary entries a warp reads at once, 8 per lane
 constexpr int kFilterBits = 8192;   // one bit per group of 8 entries (modulo): may hold a refused token
 
@@ -36,10 +51,11 @@ struct VerifyArgs {
   int32_t *accept_len, *accept_idx, *out_tokens;
   int T, V;
   int* status;
+  int cluster;                      // CTAs per sequence
 };
 
-// A probability as it counts: a negative value or a NaN is no mass.
-__device__ __forceinline__ float clean(float p) { return p > 0.f ? p : 0.f; }
+// A probability as it counts: a negative value, an infinity or a NaN is no mass.
+__device__ __forceinline__ float clean(float p) { return p > 0.f && p < INFINITY ? p : 0.f; }
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
 
@@ -77,21 +93,49 @@ struct Residual {
   const uint32_t* filter;
 };
 
+// An unevaluated sum of two fp32 values, hi the sum rounded.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_diff(float a, float b) {     // a - b, exactly
+  const float d = a - b, t = d - a;
+  return {d, (a - (d - t)) - (b + t)};
+}
+__device__ __forceinline__ void add_to(Pair& s, Pair v) {
+  const float t = s.hi + v.hi, b = t - s.hi;
+  s.lo += ((s.hi - (t - b)) + (v.hi - b)) + v.lo;
+  s.hi = t;
+}
+__device__ __forceinline__ double value(Pair v) { return (double)v.hi + (double)v.lo; }
+
+// Entries [x, x + 8) of what is left.
 template <typename T>
 __device__ __forceinline__ void residual8(const T* p_row, const T* q_row, const Residual& r, int x, int V,
-                                          double (&out)[8]) {
+                                          Pair (&out)[8]) {
   float p[8];
   load8(p_row, x, V, p);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) out[e] = (double)clean(p[e]);
   if (r.C > 0.0) {
     float q[8];
     load8(q_row, x, V, q);
+    if (r.C == 1.0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double d = out[e] - r.C * (double)clean(q[e]);
-      out[e] = d > 0.0 ? d : 0.0;
+      for (int e = 0; e < 8; ++e) out[e] = two_diff(clean(p[e]), clean(q[e]));
+    } else {
+      const float ch = (float)r.C, cl = (float)(r.C - (double)ch);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float qe = clean(q[e]), h = ch * qe, l = fmaf(cl, qe, fmaf(ch, qe, -h));
+        const Pair d = two_diff(clean(p[e]), h);
+        const float lo = d.lo - l, hi = d.hi + lo;
+        out[e] = {hi, lo - (hi - d.hi)};
+      }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!(out[e].hi > 0.f)) out[e] = {0.f, 0.f};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = {clean(p[e]), 0.f};
   }
   if (r.num_refused > 0) {
     const int bit = (x >> 3) & (kFilterBits - 1);
@@ -100,57 +144,75 @@ __device__ __forceinline__ void residual8(const T* p_row, const T* q_row, const 
         const int e = r.refused[k] - x;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (e == j) out[j] = 0.0;
+          if (e == j) out[j] = {0.f, 0.f};
       }
     }
   }
 }
 
-// Tiles [first, last) of warp w: the row is cut into contiguous runs of tiles.
-__device__ __forceinline__ void warp_tiles(int V, int w, int* first, int* last) {
-  const int n = (V + kTile - 1) / kTile;
-  *first = (int)((long long)n * w / kVerifyWarps);
-  *last = (int)((long long)n * (w + 1) / kVerifyWarps);
+// Part k of n of the tiles [t0, t1): contiguous, in order.
+__device__ __forceinline__ void part_of(int t0, int t1, int k, int n, int* first, int* last) {
+  const long long len = t1 - t0;
+  *first = t0 + (int)(len * k / n);
+  *last = t0 + (int)(len * (k + 1) / n);
 }
 
-// The mass of each warp's run into wsum[], and the whole mass (every thread).
+// The masses of the warps' parts of the tiles [t0, t1) into wsum[] (the whole CTA).
 template <typename T>
-__device__ double block_mass(const T* p_row, const T* q_row, const Residual& r, int V, double* wsum) {
+__device__ void part_masses(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1, double* wsum) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int t0, t1;
-  warp_tiles(V, w, &t0, &t1);
-  double s = 0.0;
-  for (int t = t0; t < t1; ++t) {
-    double v[8];
+  int first, last;
+  part_of(t0, t1, w, kVerifyWarps, &first, &last);
+  Pair s{0.f, 0.f};
+#pragma unroll 2
+  for (int t = first; t < last; ++t) {
+    Pair v[8];
     residual8(p_row, q_row, r, t * kTile + 8 * lane, V, v);
-    s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int e = 0; e < 8; ++e) add_to(s, v[e]);
+  }
+  double d = value(s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   __syncthreads();   // wsum's last readers are done
-  if (lane == 0) wsum[w] = s;
+  if (lane == 0) wsum[w] = d;
   __syncthreads();
-  double total = 0.0;
-  for (int k = 0; k < kVerifyWarps; ++k) total += wsum[k];
-  return total;
 }
 
-// One warp: the first entry of its run whose running sum, from `run` on, passes `goal`;
-// the run's last entry of positive mass if rounding leaves none (-1 if it has no mass).
+// Which of n parts with masses m[] holds the entry at which the running sum, `run` at
+// first, passes `goal`; the last part with mass if rounding leaves none (-1: no mass).
+// run becomes the sum before that part.
+__device__ __forceinline__ int find_part(const double* m, int n, double* run, double goal) {
+  int last = -1;
+  double at = *run, run_last = *run;
+  for (int k = 0; k < n; ++k) {
+    if (m[k] > 0.0) {
+      last = k;
+      run_last = at;
+      if (at + m[k] > goal) break;
+    }
+    at += m[k];
+  }
+  *run = run_last;
+  return last;
+}
+
+// One warp: the first entry of the tiles [t0, t1) whose running sum, from `run` on,
+// passes `goal`; their last entry of positive mass if rounding leaves none.
 template <typename T>
-__device__ int warp_find(const T* p_row, const T* q_row, const Residual& r, int V, int w, double run, double goal) {
+__device__ int warp_find(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1, double run,
+                         double goal) {
   const int lane = threadIdx.x & 31;
-  int t0, t1, last = -1;
-  warp_tiles(V, w, &t0, &t1);
+  int last = -1;
   for (int t = t0; t < t1; ++t) {
     const int x = t * kTile + 8 * lane;
-    double v[8];
+    Pair v[8];
     residual8(p_row, q_row, r, x, V, v);
     double s = 0.0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      s += v[e];
-      if (v[e] > 0.0) last = x + e;
+      s += value(v[e]);
+      if (v[e].hi > 0.f) last = x + e;
     }
     double incl = s;
 #pragma unroll
@@ -162,16 +224,17 @@ __device__ int warp_find(const T* p_row, const T* q_row, const Residual& r, int 
     if (hit) {
       const int src = __ffs(hit) - 1;
       int found = -1;
+      bool passed = false;
       double acc = run + (incl - s);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        acc += v[e];
-        if (v[e] > 0.0 && (found < 0 || !(found & 0x40000000))) {
-          // the first entry that passes the goal is final (marked); until then the last positive one stands
-          found = (x + e) | (acc > goal ? 0x40000000 : 0);
+        acc += value(v[e]);
+        if (v[e].hi > 0.f && !passed) {      // until one passes the goal, the last positive one stands
+          found = x + e;
+          passed = acc > goal;
         }
       }
-      return __shfl_sync(0xffffffffu, found, src) & 0x3FFFFFFF;
+      return __shfl_sync(0xffffffffu, found, src);
     }
     run += __shfl_sync(0xffffffffu, incl, 31);
   }
@@ -180,17 +243,26 @@ __device__ int warp_find(const T* p_row, const T* q_row, const Residual& r, int 
   return last;
 }
 
-// One CTA per sequence.  Every warp walks the tree alike, from shared memory; the whole
-// CTA sums a row whenever the walk asks for the mass left after a refusal.
+// What the walking warp tells the others.
+struct Walk {
+  int cur, count, nref, want_mass;
+  double C;
+};
+
+// One cluster of CTAs per sequence.
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
-  extern __shared__ int smem[];      // tokens, parents, p(x), q(x) per node; the path; refused tokens
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a) {
+  extern __shared__ int smem[];      // tokens, parents, p(x), q(x), u per node; the path; refused tokens
   __shared__ double wsum[kVerifyWarps];
+  __shared__ double slice[2][kMaxCluster];   // the CTAs' masses, by turns
   __shared__ uint32_t filter[kFilterBits / 32];
+  __shared__ Walk s_walk;
   __shared__ int s_next;
+  ptx::cluster_sync_all();   // the other CTAs run: their shared memory may be written
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)ptx::cluster_ctarank(), size = a.cluster;
+  const int b = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int N = a.T;
   int* tok = smem;
   int* par = smem + N;
@@ -200,11 +272,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
   int* path = smem + 5 * N;
   int* refused = smem + 6 * N;
   int n = a.node_lens ? a.node_lens[b] : N;
-  const bool bad_len = n < 0 || n > N;
-  if (bad_len) n = 0;
+  bool bad = n < 0 || n > N;
+  if (bad) n = 0;
   const T* target = static_cast<const T*>(a.target) + (size_t)b * N * a.row_stride;
   const T* draft = a.draft ? static_cast<const T*>(a.draft) + (size_t)b * N * a.row_stride : nullptr;
-  bool bad = bad_len;
   for (int t = tid; t < n; t += kVerifyThreads) {
     const int x = a.tokens[(size_t)b * N + t], pr = a.parents[(size_t)b * N + t];
     // A node that can be accepted hangs on an earlier one and holds a token of the vocabulary.
@@ -217,107 +288,154 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(VerifyArgs a) {
     qx[t] = fine && draft ? clean(widen(draft[(size_t)pr * a.row_stride + x])) : 1.f;
   }
   for (int k = tid; k < kFilterBits / 32; k += kVerifyThreads) filter[k] = 0;
-  if (bad) atomicCAS(a.status, 0, MLA_ERR_DEVICE_CHECK);
+  if (bad && rank == 0) atomicCAS(a.status, 0, MLA_ERR_DEVICE_CHECK);
   __syncthreads();
 
+  int t0, t1, turn = 0;
+  part_of(0, (a.V + kTile - 1) / kTile, rank, size, &t0, &t1);
+  // The mass of what is left of a row, its slices' masses in slice[turn ^ 1] afterwards.
+  auto mass = [&](const T* p_row, const T* q_row, const Residual& r) -> double {
+    part_masses(p_row, q_row, r, a.V, t0, t1, wsum);
+    if (warp == 0) {
+      double mine = 0.0;
+      for (int k = 0; k < kVerifyWarps; ++k) mine += wsum[k];
+      if (lane < size) {
+        const uint32_t to = ptx::map_to_cta(ptx::smem_addr(&slice[turn][rank]), lane);
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(mine) : "memory");
+      }
+    }
+    __syncwarp();
+    ptx::cluster_sync_all();
+    double total = 0.0;
+    for (int k = 0; k < size; ++k) total += slice[turn][k];
+    turn ^= 1;
+    return total;
+  };
+
+  // The walk (warp 0), stopping where a refusal asks for the mass left.
   int cur = 0, at = 0, count = n > 0 ? 1 : 0, nref = 0;
   double C = 0.0, Z = 1.0;
   bool stale = false;     // Z has to be summed anew
   if (tid == 0 && n > 0) path[0] = 0;
-  while (n > 0) {
-    // the next child of cur, in index order
-    int child = -1;
-    for (int base = at + 1; base < n; base += 32) {
-      const unsigned m = __ballot_sync(0xffffffffu, base + lane < n && par[base + lane] == cur);
-      if (m) { child = base + __ffs(m) - 1; break; }
-    }
-    if (child < 0) break;
-    at = child;
-    const double u = (double)ua[child], p = (double)px[child], q = (double)qx[child];
-    double left;
-    if (draft) {
-      if (stale) {
-        const Residual r{C, 0, nullptr, filter};
-        Z = block_mass(target + (size_t)cur * a.row_stride, draft + (size_t)cur * a.row_stride, r, a.V, wsum);
-        stale = false;
+  while (true) {
+    if (warp == 0) {
+      int want = 0;
+      while (n > 0) {
+        // the next child of cur, in index order
+        int child = -1;
+        for (int base = at + 1; base < n; base += 32) {
+          const unsigned m = __ballot_sync(0xffffffffu, base + lane < n && par[base + lane] == cur);
+          if (m) { child = base + __ffs(m) - 1; break; }
+        }
+        if (child < 0) break;
+        if (stale) { want = 1; break; }
+        at = child;
+        const double u = (double)ua[child], p = (double)px[child], q = (double)qx[child];
+        double left = p - C * q;
+        if (!draft) {
+          bool again = false;
+          for (int base = 0; base < nref; base += 32)
+            again |= __any_sync(0xffffffffu, base + lane < nref && refused[base + lane] == tok[child]);
+          left = again ? 0.0 : p;
+        }
+        if (left > 0.0 && u * q * Z < left) {
+          cur = child;
+          if (lane == 0) path[count] = child;
+          ++count;
+          C = 0.0; Z = 1.0; nref = 0;
+        } else if (draft) {
+          C += Z;
+          stale = true;
+        } else {
+          if (left > 0.0) Z -= left;
+          if (lane == 0) refused[nref] = tok[child];
+          ++nref;
+          __syncwarp();
+        }
       }
-      left = p - C * q;
-    } else {
-      bool again = false;
-      for (int base = 0; base < nref; base += 32)
-        again |= __any_sync(0xffffffffu, base + lane < nref && refused[base + lane] == tok[child]);
-      left = again ? 0.0 : p;
+      if (lane == 0) s_walk = Walk{cur, count, nref, want, C};
     }
-    if (left > 0.0 && u * q * Z < left) {
-      cur = child;
-      if (tid == 0) path[count] = child;
-      ++count;
-      C = 0.0; Z = 1.0; nref = 0; stale = false;
-    } else if (draft) {
-      C += Z;
-      stale = true;
-    } else {
-      if (left > 0.0) Z -= left;
-      __syncthreads();     // the list's readers are done
-      if (tid == 0) refused[nref] = tok[child];
-      ++nref;
-      __syncthreads();
+    __syncthreads();
+    const Walk w = s_walk;
+    if (!w.want_mass) break;
+    const Residual r{w.C, 0, nullptr, filter};
+    const double m = mass(target + (size_t)w.cur * a.row_stride, draft + (size_t)w.cur * a.row_stride, r);
+    if (warp == 0) {
+      Z = m;
+      stale = false;
     }
   }
-  __syncthreads();
 
-  int next = -1;
+  const Walk w = s_walk;
+  int next = -1, writer = 0;
   if (n > 0) {
-    for (int k = tid; k < nref; k += kVerifyThreads) {
+    for (int k = tid; k < w.nref; k += kVerifyThreads) {
       const int bit = (refused[k] >> 3) & (kFilterBits - 1);
       atomicOr(&filter[bit >> 5], 1u << (bit & 31));
     }
     __syncthreads();
-    const T* p_row = target + (size_t)cur * a.row_stride;
-    const T* q_row = draft ? draft + (size_t)cur * a.row_stride : nullptr;
-    Residual r{C, nref, refused, filter};
-    double total = block_mass(p_row, q_row, r, a.V, wsum);
+    const T* p_row = target + (size_t)w.cur * a.row_stride;
+    const T* q_row = draft ? draft + (size_t)w.cur * a.row_stride : nullptr;
+    Residual r{w.C, w.nref, refused, filter};
+    double total = mass(p_row, q_row, r);
     if (!(total > 0.0)) {
       // nothing is left (p lies under the drafts everywhere): the draw is from p itself
       r.C = 0.0;
       r.num_refused = 0;
-      total = block_mass(p_row, q_row, r, a.V, wsum);
+      total = mass(p_row, q_row, r);
     }
     if (total > 0.0) {
       const double goal = (double)a.u_sample[b] * total;
       double run = 0.0;
-      int w = -1, last = -1;
-      double run_w = 0.0, run_last = 0.0;
-      for (int k = 0; k < kVerifyWarps; ++k) {
-        if (wsum[k] > 0.0) { last = k; run_last = run; }
-        if (w < 0 && wsum[k] > 0.0 && run + wsum[k] > goal) { w = k; run_w = run; }
-        run += wsum[k];
+      writer = find_part(slice[turn ^ 1], size, &run, goal);   // the CTA, then its warp's part,
+      if (rank == writer) {
+        int k = find_part(wsum, kVerifyWarps, &run, goal);
+        part_of(t0, t1, k, kVerifyWarps, &t0, &t1);
+        __syncthreads();
+        part_masses(p_row, q_row, r, a.V, t0, t1, wsum);       // that part shared out again, the tile in it
+        k = find_part(wsum, kVerifyWarps, &run, goal);
+        part_of(t0, t1, k, kVerifyWarps, &t0, &t1);
+        if (warp == k) {
+          const int x = warp_find(p_row, q_row, r, a.V, t0, t1, run, goal);
+          if (lane == 0) s_next = x;
+        }
+        __syncthreads();
+        next = s_next;
       }
-      if (w < 0) { w = last; run_w = run_last; }
-      if (warp == w) {
-        const int x = warp_find(p_row, q_row, r, a.V, w, run_w, goal);
-        if (lane == 0) s_next = x;
-      }
-      __syncthreads();
-      next = s_next;
     }
   }
+  if (rank != writer) return;
   for (int t = tid; t < N; t += kVerifyThreads) {
-    a.accept_idx[(size_t)b * N + t] = t < count ? path[t] : -1;
-    a.out_tokens[(size_t)b * N + t] = t + 1 < count ? tok[path[t + 1]] : (t + 1 == count ? next : -1);
+    a.accept_idx[(size_t)b * N + t] = t < w.count ? path[t] : -1;
+    a.out_tokens[(size_t)b * N + t] = t + 1 < w.count ? tok[path[t + 1]] : (t + 1 == w.count ? next : -1);
   }
-  if (tid == 0) a.accept_len[b] = count;
+  if (tid == 0) a.accept_len[b] = w.count;
 }
 
 }  // namespace
 
 cudaError_t launch_verify_tree(const VerifyCall& c, cudaStream_t st) {
   VerifyArgs a{c.target, c.draft, c.row_stride, c.tokens, c.parents, c.node_lens, c.u_accept, c.u_sample,
-               c.accept_len, c.accept_idx, c.out_tokens, c.T, c.V, bmm_status_ptr()};
+               c.accept_len, c.accept_idx, c.out_tokens, c.T, c.V, bmm_status_ptr(), 1};
   if (!a.status) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)c.T * 7 * sizeof(int);
-  return c.bf16 ? launch_pdl(verify_kernel<__nv_bfloat16>, dim3(c.B), dim3(kVerifyThreads), smem, st, a)
-                : launch_pdl(verify_kernel<float>, dim3(c.B), dim3(kVerifyThreads), smem, st, a);
+  // As many CTAs per sequence as stay resident at once (two per SM).
+  const int slots = 2 * mla_device_sm_count();
+  while (a.cluster < kMaxCluster && (long long)c.B * a.cluster * 2 <= slots) a.cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(c.B * a.cluster));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.dynamicSmemBytes = (size_t)c.T * 7 * sizeof(int);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return c.bf16 ? cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, a)
+                : cudaLaunchKernelEx(&cfg, verify_kernel<float>, a);
 }
 
 }  // namespace mla

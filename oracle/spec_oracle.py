@@ -54,7 +54,7 @@ def verify_ref(target, draft, tokens, parents, n, u_accept, u_sample):
     if n == 0:
         return [], -1
     V = target.shape[1]
-    mass = lambda x: np.where(x > 0, x, 0.0)  # noqa: E731  (negative values and NaN are no mass)
+    mass = lambda x: np.where((x > 0) & (x < np.inf), x, 0.0)  # noqa: E731
     path, cur = [0], 0
     left, Z = mass(target[0]), 1.0      # what is left of cur's row, unnormalised, and its mass
     for t in range(1, n):

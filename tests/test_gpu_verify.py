@@ -169,13 +169,15 @@ def test_verify_borders(mla, cuda):
 
 
 def test_verify_rows_without_mass_and_odd_values(mla, cuda):
-    """Rows of zeros give -1; NaN and negative probabilities are no mass; q may be anything where no child hangs."""
+    """Rows of zeros give -1; NaN, infinite and negative probabilities are no mass; q may be anything where no child hangs."""
     import torch
     V = 700
     g = torch.Generator(device="cuda").manual_seed(2)
     p, q = _probs(torch, g, 4, 3, V, torch.float32)
     p[0] = 0
     p[1, :, ::2] = float("nan")
+    p[1, :, 1::10] = float("inf")
+    q[1, :, 5::10] = float("inf")
     p[2, :, 5:] *= -1
     q[:, 2] = float("nan")
     tokens = [[0, 4, 8], [0, 3, 9], [0, 2, 1], [0, 1, 2]]
