@@ -106,6 +106,14 @@ __device__ __forceinline__ void add_to(Pair& s, Pair v) {
   s.lo += ((s.hi - (t - b)) + (v.hi - b)) + v.lo;
   s.hi = t;
 }
+__device__ __forceinline__ Pair shfl_xor(Pair v, int o) {
+  return {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)};
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 __device__ __forceinline__ double value(Pair v) { return (double)v.hi + (double)v.lo; }
 
 // Entries [x, x + 8) of what is left.
@@ -159,7 +167,7 @@ __device__ __forceinline__ void part_of(int t0, int t1, int k, int n, int* first
 
 // The masses of the warps' parts of the tiles [t0, t1) into wsum[] (the whole CTA).
 template <typename T>
-__device__ void part_masses(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1, double* wsum) {
+__device__ void part_masses(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1, Pair* wsum) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int first, last;
   part_of(t0, t1, w, kVerifyWarps, &first, &last);
@@ -171,30 +179,29 @@ __device__ void part_masses(const T* p_row, const T* q_row, const Residual& r, i
 #pragma unroll
     for (int e = 0; e < 8; ++e) add_to(s, v[e]);
   }
-  double d = value(s);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  for (int o = 16; o > 0; o >>= 1) add_to(s, shfl_xor(s, o));
   __syncthreads();   // wsum's last readers are done
-  if (lane == 0) wsum[w] = d;
+  if (lane == 0) wsum[w] = s;
   __syncthreads();
 }
 
-// Which of n parts with masses m[] holds the entry at which the running sum, `run` at
-// first, passes `goal`; the last part with mass if rounding leaves none (-1: no mass).
-// run becomes the sum before that part.
-__device__ __forceinline__ int find_part(const double* m, int n, double* run, double goal) {
-  int last = -1;
-  double at = *run, run_last = *run;
-  for (int k = 0; k < n; ++k) {
-    if (m[k] > 0.0) {
-      last = k;
-      run_last = at;
-      if (at + m[k] > goal) break;
-    }
-    at += m[k];
+// One warp, lane k holding the mass m of part k (0 past the last): the part that holds
+// the entry at which the running sum, `run` at first, passes `goal`; the last part with
+// mass if rounding leaves none (-1: no mass).  run becomes the sum before that part.
+__device__ __forceinline__ int find_part(double m, double* run, double goal) {
+  const int lane = threadIdx.x & 31;
+  double incl = m;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
-  *run = run_last;
-  return last;
+  const unsigned some = __ballot_sync(0xffffffffu, m > 0.0);
+  const unsigned hit = __ballot_sync(0xffffffffu, m > 0.0 && *run + incl > goal);
+  const int k = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+  if (k >= 0) *run += __shfl_sync(0xffffffffu, incl - m, k);
+  return k;
 }
 
 // One warp: the first entry of the tiles [t0, t1) whose running sum, from `run` on,
@@ -205,38 +212,29 @@ __device__ int warp_find(const T* p_row, const T* q_row, const Residual& r, int 
   const int lane = threadIdx.x & 31;
   int last = -1;
   for (int t = t0; t < t1; ++t) {
-    const int x = t * kTile + 8 * lane;
-    Pair v[8];
-    residual8(p_row, q_row, r, x, V, v);
-    double s = 0.0;
+    Pair v[8], s{0.f, 0.f};
+    residual8(p_row, q_row, r, t * kTile + 8 * lane, V, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      s += value(v[e]);
-      if (v[e].hi > 0.f) last = x + e;
+      add_to(s, v[e]);
+      if (v[e].hi > 0.f) last = t * kTile + 8 * lane + e;
     }
-    double incl = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, run + incl > goal && s > 0.0);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      int found = -1;
-      bool passed = false;
-      double acc = run + (incl - s);
+    double before = run;
+    const double mine = value(s);
+    int src = find_part(mine, &before, goal);
+    // the lane found passes the goal, or is the last one with mass of a tile that does not
+    const double after = before + __shfl_sync(0xffffffffu, mine, src < 0 ? 0 : src);
+    if (src >= 0 && after > goal) {
+      // its eight entries, one per lane
+      Pair e8{0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        acc += value(v[e]);
-        if (v[e].hi > 0.f && !passed) {      // until one passes the goal, the last positive one stands
-          found = x + e;
-          passed = acc > goal;
-        }
+        const Pair x{__shfl_sync(0xffffffffu, v[e].hi, src), __shfl_sync(0xffffffffu, v[e].lo, src)};
+        if (lane == e) e8 = x;
       }
-      return __shfl_sync(0xffffffffu, found, src);
+      return t * kTile + 8 * src + find_part(value(e8), &before, goal);
     }
-    run += __shfl_sync(0xffffffffu, incl, 31);
+    if (src >= 0) run = after;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
@@ -249,15 +247,22 @@ struct Walk {
   double C;
 };
 
+// What warp 0 decides about the draw: the CTA (-1: nothing is left) and its warp's part.
+struct Draw {
+  int cta, part;
+  double run, goal;
+};
+
 // One cluster of CTAs per sequence.
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a) {
   extern __shared__ int smem[];      // tokens, parents, p(x), q(x), u per node; the path; refused tokens
-  __shared__ double wsum[kVerifyWarps];
+  __shared__ Pair wsum[kVerifyWarps];
   __shared__ double slice[2][kMaxCluster];   // the CTAs' masses, by turns
   __shared__ uint32_t filter[kFilterBits / 32];
   __shared__ Walk s_walk;
   __shared__ int s_next;
+  __shared__ Draw s_draw;
   ptx::cluster_sync_all();   // the other CTAs run: their shared memory may be written
   pdl_wait();
   pdl_trigger();
@@ -293,12 +298,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
 
   int t0, t1, turn = 0;
   part_of(0, (a.V + kTile - 1) / kTile, rank, size, &t0, &t1);
-  // The mass of what is left of a row, its slices' masses in slice[turn ^ 1] afterwards.
+  // The mass of what is left of a row: lane k of warp 0 gets the mass of CTA k's slice
+  // (fp64 from here on is one warp's: an instruction takes its pipe for 16 cycles).
   auto mass = [&](const T* p_row, const T* q_row, const Residual& r) -> double {
     part_masses(p_row, q_row, r, a.V, t0, t1, wsum);
     if (warp == 0) {
-      double mine = 0.0;
-      for (int k = 0; k < kVerifyWarps; ++k) mine += wsum[k];
+      const double mine = warp_sum(lane < kVerifyWarps ? value(wsum[lane]) : 0.0);
       if (lane < size) {
         const uint32_t to = ptx::map_to_cta(ptx::smem_addr(&slice[turn][rank]), lane);
         asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(mine) : "memory");
@@ -306,10 +311,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
     }
     __syncwarp();
     ptx::cluster_sync_all();
-    double total = 0.0;
-    for (int k = 0; k < size; ++k) total += slice[turn][k];
+    const double m = warp == 0 && lane < size ? slice[turn][lane] : 0.0;
     turn ^= 1;
-    return total;
+    return m;
   };
 
   // The walk (warp 0), stopping where a refusal asks for the mass left.
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
     const Residual r{w.C, 0, nullptr, filter};
     const double m = mass(target + (size_t)w.cur * a.row_stride, draft + (size_t)w.cur * a.row_stride, r);
     if (warp == 0) {
-      Z = m;
+      Z = warp_sum(m);
       stale = false;
     }
   }
@@ -377,31 +381,41 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
     const T* p_row = target + (size_t)w.cur * a.row_stride;
     const T* q_row = draft ? draft + (size_t)w.cur * a.row_stride : nullptr;
     Residual r{w.C, w.nref, refused, filter};
-    double total = mass(p_row, q_row, r);
-    if (!(total > 0.0)) {
+    // Warp 0 decides: the CTA whose slice holds the drawn token, and the part of it.
+    auto decide = [&](double m) {
+      if (warp == 0) {
+        const double total = warp_sum(m);
+        Draw d{-1, -1, 0.0, (double)a.u_sample[b] * total};
+        if (total > 0.0) {
+          d.cta = find_part(m, &d.run, d.goal);
+          if (d.cta == rank) d.part = find_part(lane < kVerifyWarps ? value(wsum[lane]) : 0.0, &d.run, d.goal);
+        }
+        if (lane == 0) s_draw = d;
+      }
+      __syncthreads();
+    };
+    decide(mass(p_row, q_row, r));
+    if (s_draw.cta < 0 && (r.C > 0.0 || r.num_refused > 0)) {
       // nothing is left (p lies under the drafts everywhere): the draw is from p itself
       r.C = 0.0;
       r.num_refused = 0;
-      total = mass(p_row, q_row, r);
+      const double m = mass(p_row, q_row, r);
+      decide(m);
     }
-    if (total > 0.0) {
-      const double goal = (double)a.u_sample[b] * total;
-      double run = 0.0;
-      writer = find_part(slice[turn ^ 1], size, &run, goal);   // the CTA, then its warp's part,
-      if (rank == writer) {
-        int k = find_part(wsum, kVerifyWarps, &run, goal);
+    if (s_draw.cta >= 0) writer = s_draw.cta;
+    if (s_draw.cta == rank) {
+      part_of(t0, t1, s_draw.part, kVerifyWarps, &t0, &t1);
+      part_masses(p_row, q_row, r, a.V, t0, t1, wsum);       // that part shared out again, and the token in it
+      if (warp == 0) {
+        double run = s_draw.run;
+        const double goal = s_draw.goal;
+        const int k = find_part(lane < kVerifyWarps ? value(wsum[lane]) : 0.0, &run, goal);
         part_of(t0, t1, k, kVerifyWarps, &t0, &t1);
-        __syncthreads();
-        part_masses(p_row, q_row, r, a.V, t0, t1, wsum);       // that part shared out again, the tile in it
-        k = find_part(wsum, kVerifyWarps, &run, goal);
-        part_of(t0, t1, k, kVerifyWarps, &t0, &t1);
-        if (warp == k) {
-          const int x = warp_find(p_row, q_row, r, a.V, t0, t1, run, goal);
-          if (lane == 0) s_next = x;
-        }
-        __syncthreads();
-        next = s_next;
+        const int x = warp_find(p_row, q_row, r, a.V, t0, t1, run, goal);
+        if (lane == 0) s_next = x;
       }
+      __syncthreads();
+      next = s_next;
     }
   }
   if (rank != writer) return;
