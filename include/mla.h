@@ -264,7 +264,13 @@ mla_status mla_decode_sparse(const mla_geom* geom, const mla_batch* batch, const
  * mla_plan_tree stands in for mla_plan (the same workspace and size), and is re-run
  * when the lengths or node counts change; the mask is the decode's alone.  checked, the
  * status word and every other argument as for mla_decode and mla_decode_fp8.
+ * mla_decode_tree_fp8 given mla_tree_fp8_workspace_size() bytes (0 on invalid
+ * arguments; as much as the batch's longest table as bf16 rows on top of the plan's)
+ * converts each page once, ahead of the attention, where a sequence has more than 128
+ * query rows (T * H > 128): about twice as fast as with mla_workspace_size() bytes,
+ * with which every 128 rows convert the pages they read.
  */
+size_t mla_tree_fp8_workspace_size(const mla_geom* geom, const mla_batch* batch);
 mla_status mla_plan_tree(const mla_geom* geom, const mla_batch* batch, const int32_t* seq_lens,
                          const int32_t* node_lens, void* workspace, size_t ws_bytes, mla_stream_t stream);
 mla_status mla_decode_tree(const mla_geom* geom, const mla_batch* batch, const void* q_lat, const void* q_pe,

@@ -90,6 +90,7 @@ def _load() -> ctypes.CDLL:
         "mla_normal_chunk_bytes": (ctypes.c_size_t, [G, I, I]),
         "mla_normal_chunk_state_bytes": (ctypes.c_size_t, [G, Bt]),
         "mla_normal_chunked": (I, [G, Bt, P, P, C, P, I, P, P, P, I, P, P, P, P, P]),
+        "mla_tree_fp8_workspace_size": (ctypes.c_size_t, [G, Bt]),
         "mla_plan_tree": (I, [G, Bt, P, P, P, ctypes.c_size_t, P]),
         "mla_decode_tree": (I, [G, Bt, P, P, C, P, I, P, P, P, I, P, P, P, ctypes.c_size_t, P]),
         "mla_decode_tree_fp8": (I, [G, Bt, P, P, P, I, P, I, P, P, P, I, P, P, P, ctypes.c_size_t, P]),
@@ -119,7 +120,7 @@ EXPORTED = ("mla_workspace_size", "mla_plan", "mla_absorb_q", "mla_unabsorb_o", 
             "mla_split_merge", "mla_normal_rows_per_seq", "mla_normal_expanded_bytes", "mla_normal_expand",
             "mla_normal_attention", "mla_normal_chunk_bytes", "mla_normal_chunk_state_bytes", "mla_normal_chunked",
             "mla_rope_append", "mla_rope_append_fp8", "mla_verify_tree",
-            "mla_plan_tree", "mla_decode_tree", "mla_decode_tree_fp8",
+            "mla_tree_fp8_workspace_size", "mla_plan_tree", "mla_decode_tree", "mla_decode_tree_fp8",
             "mla_cache_compact", "mla_cache_compact_fp8", "mla_pages_resize", "mla_pages_fork", "mla_cache_copy",
             "mla_cache_copy_fp8",
             "mla_fp8_pack_cache", "mla_debug_gather", "mla_debug_set_wait_limit", "mla_read_device_status",
@@ -311,6 +312,11 @@ def mla_normal_chunked(geom, batch, q_nope, q_pe, cache: mla_cache, block_table,
                                    ctypes.byref(cache), _ptr(block_table), bt_stride, _ptr(seq_lens), _ptr(w_uk),
                                    _ptr(w_uv), int(chunk_rows), _ptr(kv_chunk), _ptr(state), _ptr(o), _ptr(lse),
                                    _stream(stream))
+
+
+def mla_tree_fp8_workspace_size(geom: mla_geom, batch: mla_batch) -> int:
+    """Workspace with which mla_decode_tree_fp8 converts each page once (mla_workspace_size is enough to run)."""
+    return int(_lib.mla_tree_fp8_workspace_size(ctypes.byref(geom), ctypes.byref(batch)))
 
 
 def mla_plan_tree(geom, batch, seq_lens, node_lens, workspace, ws_bytes: int, stream=None) -> int:

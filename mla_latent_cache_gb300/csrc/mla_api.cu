@@ -282,6 +282,28 @@ mla_status mla_decode_tree(const mla_geom* geom, const mla_batch* batch, const v
                                          (cudaStream_t)stream, nullptr, nullptr, &tree));
 }
 
+// Where an FP8 tree decode keeps converted pages: past the plan's workspace, a block
+// table, then a bf16 pool of B * max_pages blocks.  False where converting ahead does
+// not pay (one row group per sequence converts each page once as it is) or has no room.
+static bool tree_scratch(const mla_geom* g, const mla_batch* b, size_t plan_bytes, size_t* table, size_t* pool,
+                         size_t* total) {
+  const long long blocks = (long long)b->B * b->max_pages;
+  *total = plan_bytes;
+  if ((long long)b->T * g->H <= kRowsPerBlock || b->B > 65535 || blocks * kPage >= (1LL << 31)) return false;
+  *table = plan_bytes;
+  *pool = align_up(*table + (size_t)blocks * sizeof(int32_t));
+  *total = *pool + (size_t)blocks * kPage * kDK * sizeof(__nv_bfloat16);
+  return true;
+}
+
+size_t mla_tree_fp8_workspace_size(const mla_geom* geom, const mla_batch* batch) {
+  const size_t plan = mla_workspace_size(geom, batch);
+  if (plan == 0 || batch->causal || batch->T > kMaxTreeNodes) return 0;
+  size_t table, pool, total;
+  tree_scratch(geom, batch, plan, &table, &pool, &total);
+  return total;
+}
+
 mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, const void* q_lat, const void* q_pe,
                                const void* cache_fp8, int num_blocks, const int32_t* block_table, int bt_stride,
                                const int32_t* seq_lens, const int32_t* node_lens, const uint32_t* tree_mask,
@@ -308,6 +330,25 @@ mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, con
   cv.num_blocks = num_blocks;
   const Fp8Pool pool{static_cast<const unsigned char*>(cache_fp8), num_blocks};
   const TreeNodes tree{node_lens, tree_mask};
+  size_t off_table, off_pool, total;
+  if (tree_scratch(geom, batch, L.total, &off_table, &off_pool, &total) && ws_bytes >= total) {
+    // each page converted once, then the decode over bf16 pages
+    char* base = static_cast<char*>(workspace);
+    int32_t* table = reinterpret_cast<int32_t*>(base + off_table);
+    __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(base + off_pool);
+    if (launch_fp8_expand(pool, block_table, bt_stride, batch->B, batch->max_pages, seq_lens, checked, workspace,
+                          table, rows, (cudaStream_t)stream) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    cv.ckv = rows;
+    cv.kpe = rows + kDLat;
+    cv.ckv_row = cv.kpe_row = kDK;
+    cv.ckv_block = cv.kpe_block = (int64_t)kPage * kDK;
+    cv.num_blocks = batch->B * batch->max_pages;
+    return cuda_status(launch_decode_sm103(geom, batch, L, static_cast<const __nv_bfloat16*>(q_lat),
+                                           static_cast<const __nv_bfloat16*>(q_pe), cv, table, batch->max_pages,
+                                           seq_lens, checked, static_cast<__nv_bfloat16*>(o_lat), lse, workspace,
+                                           (cudaStream_t)stream, nullptr, nullptr, &tree));
+  }
   return cuda_status(launch_decode_sm103(geom, batch, L, static_cast<const __nv_bfloat16*>(q_lat),
                                          static_cast<const __nv_bfloat16*>(q_pe), cv, block_table, bt_stride,
                                          seq_lens, checked, static_cast<__nv_bfloat16*>(o_lat), lse, workspace,

@@ -1,5 +1,5 @@
-// The FP8 cache row's quantisation (the row and its rule are described in
-// mla_fp8.cu), shared by the kernels that write such rows.
+// The FP8 cache row's quantisation and its inverse (the row and its rule are described
+// in mla_fp8.cu), shared by the kernels that write and read such rows.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -37,6 +37,40 @@ __device__ __forceinline__ uint32_t e4m3_nearest(float x, float scale) {
     if (r > 0.f || (r == 0.f && (c & 1u))) c -= 1;
   }
   return sign | c;
+}
+
+// Four E4M3 codes (the lowest byte first) times the tile's scale, as two bf16
+// pairs: each code is widened exactly (to f16 by the E4M3 conversion, two codes
+// per instruction, to fp32 by a mixed-precision multiply-add with 1), each pair
+// multiplied by the fp32 scale in one packed multiply (each lane rounded to
+// nearest, as two scalar multiplies), and the products rounded to bf16
+// (measured faster than building the fp32 bits with integer operations).
+// scale2: the scale in both halves.
+__device__ __forceinline__ uint2 dequant4(uint32_t four, uint64_t scale2) {
+  uint2 r;
+  asm("{\n\t.reg .b16 c0, c1, l0, u0, l1, u1, one;\n\t.reg .b32 h0, h1;\n\t.reg .f32 a0, b0, a1, b1;\n\t"
+      ".reg .b64 p0, p1;\n\t"
+      "mov.b16 one, 0x3C00;\n\t"
+      "mov.b32 {c0, c1}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h0, c0;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h1, c1;\n\t"
+      "mov.b32 {l0, u0}, h0;\n\t"
+      "mov.b32 {l1, u1}, h1;\n\t"
+      "fma.rn.f32.f16 a0, l0, one, 0f00000000;\n\t"
+      "fma.rn.f32.f16 b0, u0, one, 0f00000000;\n\t"
+      "fma.rn.f32.f16 a1, l1, one, 0f00000000;\n\t"
+      "fma.rn.f32.f16 b1, u1, one, 0f00000000;\n\t"
+      "mov.b64 p0, {a0, b0};\n\t"
+      "mov.b64 p1, {a1, b1};\n\t"
+      "mul.rn.f32x2 p0, p0, %3;\n\t"
+      "mul.rn.f32x2 p1, p1, %3;\n\t"
+      "mov.b64 {a0, b0}, p0;\n\t"
+      "mov.b64 {a1, b1}, p1;\n\t"
+      "cvt.rn.bf16x2.f32 %0, b0, a0;\n\t"
+      "cvt.rn.bf16x2.f32 %1, b1, a1;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(four), "l"(scale2));
+  return r;
 }
 
 // A warp's 512 latent values as E4M3 codes: lane l holds values [16 l, 16 l + 16)

@@ -131,6 +131,10 @@ cudaError_t launch_decode_sm103(const mla_geom* g, const mla_batch* b, const WsL
                                 const SparseList* sparse = nullptr, const Fp8Pool* fp8 = nullptr,
                                 const TreeNodes* tree = nullptr);
 int decode_sm103_pairs_per_device();
+// FP8 pages as bf16 pages of a scratch pool [B * max_pages, 64, 576], and its block table [B, max_pages].
+cudaError_t launch_fp8_expand(const Fp8Pool& pool, const int32_t* block_table, int bt_stride, int B, int max_pages,
+                              const int32_t* seq_lens, int checked, void* ws, int32_t* table, void* out,
+                              cudaStream_t st);
 cudaError_t launch_split_merge(const float* part_o, const float* part_lse, const int32_t* indptr, int M,
                                int rows, int D, __nv_bfloat16* o, float* lse, cudaStream_t st);
 cudaError_t launch_absorb_sm103(const __nv_bfloat16* q_nope, const __nv_bfloat16* w_uk, __nv_bfloat16* q_lat,

@@ -18,7 +18,7 @@ class Tree:
     """One batch: a workload of the decode's recipe (NaN past every sequence's end) and a mask."""
 
     def __init__(self, mla, torch, cuda, H, lens, T, nodes=None, see=None, seed=7, sharp=True, fp8=False, slots=0,
-                 override=0, split=False):
+                 override=0, split=False, ahead=True):
         from mla_latent_cache_gb300.runtime import _u16_to_bf16, pool_to_device
         self.mla, self.torch = mla, torch
         w = self.w = W.custom_workload(H, lens, T=T, seed=seed, sharp=sharp)
@@ -50,7 +50,9 @@ class Tree:
         self.q_lat, self.q_pe = _u16_to_bf16(torch, w.q_lat, cuda), _u16_to_bf16(torch, w.q_pe, cuda)
         self.o = torch.full((B, T, H, 512), float("nan"), dtype=torch.bfloat16, device=cuda)
         self.lse = torch.full((B, T, H), float("nan"), dtype=torch.float32, device=cuda)
-        self.ws_bytes = mla.mla_workspace_size(self.geom, self.batch)
+        # FP8: room to convert the pages ahead, or (ahead=False) as much as the plan needs
+        size = mla.mla_tree_fp8_workspace_size if fp8 and ahead else mla.mla_workspace_size
+        self.ws_bytes = size(self.geom, self.batch)
         self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=cuda)
 
     def plan(self):
@@ -157,6 +159,22 @@ def test_unseen_rows_may_hold_anything(mla, cuda, H, fp8):
             else:
                 t.pool[blk, j % 64] = v
     t.run().check()
+
+
+@pytest.mark.parametrize("H,lens,T,nodes", [(128, [70, 300, 0, 131, 2000], 17, [17, 3, 0, 9, 17]),
+                                              (16, [64, 1000, 65], 20, None)])
+def test_fp8_pages_converted_ahead_or_by_each_group(mla, cuda, H, lens, T, nodes):
+    """The same values either way (equal bits: the same products, rounded alike, in the same schedule)."""
+    import torch
+    a = Tree(mla, torch, cuda, H, lens, T, nodes=nodes, fp8=True, sharp=False).run().check()
+    b = Tree(mla, torch, cuda, H, lens, T, nodes=nodes, fp8=True, sharp=False, ahead=False).run().check()
+    assert a.ws_bytes > b.ws_bytes
+    assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse)
+    # a block outside the pool reads as zeros and is reported, converted ahead too
+    for t in (a, b):
+        t.bt[1, 0] = t.w.num_blocks
+        t.run(expect=mla.MLA_ERR_DEVICE_CHECK)
+    assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse)
 
 
 def test_chain_is_the_causal_decode(mla, cuda):

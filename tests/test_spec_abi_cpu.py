@@ -157,6 +157,14 @@ def test_tree_decode_refusals(mla):
         assert call(lens=None) == mla.MLA_ERR_ARG
         for name in ("lens", "nodes"):
             assert call(**{name: 0x10004}) == mla.MLA_ERR_ALIGN, name
+    # FP8 pages converted ahead: B * max_pages bf16 pages and their table, where T * H > 128
+    assert mla.mla_tree_fp8_workspace_size(g, b) == ws
+    b2 = mla.make_batch(2, 9, False, 8, num_slots=4)
+    assert mla.mla_tree_fp8_workspace_size(g, b2) == mla.mla_workspace_size(g, b2) + 256 + 2 * 8 * 64 * 1152
+    for bad in (mla.make_batch(2, 9, True, 8, num_slots=4), mla.make_batch(2, 1025, False, 8, num_slots=4),
+                mla.make_batch(2, 0, False, 8, num_slots=4)):
+        assert mla.mla_tree_fp8_workspace_size(g, bad) == 0
+    assert mla.mla_tree_fp8_workspace_size(mla.make_geom(24), b) == 0
     for call in (dec, dec8):
         assert call(batch=mla.make_batch(0, 8, False, 8, num_slots=4)) == mla.MLA_OK
         for name in ("q_lat", "q_pe", "bt", "mask", "o", "lse"):
