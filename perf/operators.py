@@ -263,7 +263,8 @@ def _handles_tree(s, L):
     c = s["case"]
     s["geom"] = L.make_geom(c["H"])
     s["batch"] = L.make_batch(c["B"], c["T"], False, s["block_table"].shape[1])
-    s["ws_bytes"] = L.mla_workspace_size(s["geom"], s["batch"])
+    size = L.mla_tree_fp8_workspace_size if c["fp8"] else L.mla_workspace_size
+    s["ws_bytes"] = size(s["geom"], s["batch"])
     s["workspace"] = torch.zeros(s["ws_bytes"], dtype=torch.uint8, device=DEV)
     if not c["fp8"]:
         s["cache"] = L.cache_from_pool(s["pool"])
