@@ -103,8 +103,11 @@ using namespace ptx;
 constexpr int kModeDense = 0, kModeSparse = 1, kModeFp8 = 2;
 constexpr int kThreads = 384;   // a multiple of 128 (the merge's thread groups)
 constexpr int kFp8Threads = 512;  // plus four converter warps (12..15) in the FP8 mode
-template <int kMode>
-__host__ __device__ constexpr int threads_of() { return kMode == kModeFp8 ? kFp8Threads : kThreads; }
+constexpr int kQueryThreads = 512;  // plus four query warps (12..15) in the tree decode of bf16 pages
+template <int kMode, bool kTree>
+__host__ __device__ constexpr int threads_of() {
+  return kMode == kModeFp8 ? kFp8Threads : kTree ? kQueryThreads : kThreads;
+}
 constexpr int kCtaRows = 64;                   // query rows per CTA
 constexpr int kHalfRows = 32;                  // page rows loaded by each CTA
 constexpr int kBoxes = 9;                      // 8 latent boxes + 1 RoPE box per cached row
@@ -884,15 +887,110 @@ __device__ __forceinline__ void reload_role(const Shared& sh, const CUtensorMap*
 // (tm_aux) bytes wide, 32 rows high, and tm_kpe the rows' RoPE values as bf16
 // (64 x 32 boxes, 128-byte swizzled); tm_page unused.  tm_aux is unused by the
 // other modes.
+// Query warps (warps 12..15 of the tree decode of bf16 pages): every segment's query into
+// tensor memory (columns 0..383: warp w its 32 lanes, all six boxes) and shared memory,
+// as soon as Q K^T of the previous segment is done with it, so that the next segment's
+// first scores are there when the softmax warps have written the last one out.  A tree at
+// 128 heads is one short segment per node; with the softmax warps staging the query
+// themselves a segment change took ~14,000 cycles from the last scores to the next ones,
+// with these warps see the launcher.  The first half of the rows is read ahead, into
+// registers.
+__device__ __forceinline__ void query_load(const FastArgs& a, const __nv_bfloat16* row, bool valid, int first,
+                                           uint32_t (&v)[3][32]) {
+#pragma unroll
+  for (int bb = 0; bb < 3; ++bb) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      uint32_t* d = v[bb] + e;
+      if (valid)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
+                     : "l"(row + 64 * (first + bb) + 2 * e));
+      else
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = 0;
+    }
+  }
+}
+__device__ __forceinline__ void query_role(const Shared& sh, const unsigned char* smem, uint32_t tmem,
+                                           const CUtensorMap* tm_qlat, const CUtensorMap* tm_qpe, const FastArgs& a,
+                                           int* hdr, volatile int* abort_flag, const int* seg, SegWalk walk, int rank,
+                                           int R, int warp, int lane) {
+  const int ln = 32 * (warp & 3) + lane, hr = ln & 63;
+  const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmemQ;
+  int sc = 0;
+  bool ok = true, in_flight = false;
+  for (int si = walk.cur(); ok && si >= 0; walk.advance(), si = walk.cur(), ++sc) {
+    const int* rec = seg + (size_t)si * kSegWords;
+    const int b = rec[0], rb = rec[1];
+    const int row0 = b * R + rb * kRowsPerBlock + kCtaRows * rank;
+    const bool valid = rb * kRowsPerBlock + kCtaRows * rank + hr < R;
+    const __nv_bfloat16* row = a.q_lat + ((size_t)row0 + hr) * kDLat;
+    uint32_t v[3][32];
+    if (sc == 0) {
+      // The first query comes with the loader's copies, by way of ring stages 3 and 4:
+      // row hr of box k, 16-byte chunk c at k * 8 KB + 128 hr + 16 (c ^ (hr % 8)).
+      in_flight = true;
+      if (!warp_wait(sh.bar(BAR_Q_TMA), 0, abort_flag, hdr, 50)) { ok = false; break; }
+      in_flight = false;
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int bb = 0; bb < 3; ++bb) {
+          const unsigned char* box =
+              smem + kSmemRing + kQStageFirst * kStageBytes + (3 * half + bb) * kQBoxBytes + hr * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(box + 16 * (c ^ (hr & 7)));
+            v[bb][4 * c] = x.x; v[bb][4 * c + 1] = x.y; v[bb][4 * c + 2] = x.z; v[bb][4 * c + 3] = x.w;
+          }
+        }
+#pragma unroll
+        for (int bb = 0; bb < 3; ++bb) tmem_st32(t_lane + 32 * (3 * half + bb), v[bb]);
+      }
+      tmem_wait_st();
+      // the staging area goes back to the page ring (its reads precede the page loads' writes)
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.bar(BAR_Q_COPIED));
+    } else {
+      query_load(a, row, valid, 0, v);
+      if (!warp_wait(sh.bar(BAR_Q_FREE), (sc - 1) & 1, abort_flag, hdr, 51)) { ok = false; break; }
+      tc_fence_after();
+      if (warp == 12 && lane == 0) {
+        mbar_arrive_expect_tx(sh.bar(BAR_Q_TMA), kQSmemBoxes * kQBoxBytes);
+        for (int box = kQTmemBoxes; box < 8; ++box) tma_load_2d(sh.q(box), tm_qlat, sh.bar(BAR_Q_TMA), 64 * box, row0);
+        tma_load_2d(sh.q(8), tm_qpe, sh.bar(BAR_Q_TMA), 0, row0);
+      }
+      __syncwarp();
+      in_flight = true;
+#pragma unroll
+      for (int bb = 0; bb < 3; ++bb) tmem_st32(t_lane + 32 * bb, v[bb]);
+      query_load(a, row, valid, 3, v);
+#pragma unroll
+      for (int bb = 0; bb < 3; ++bb) tmem_st32(t_lane + 32 * (3 + bb), v[bb]);
+      tmem_wait_st();
+      if (!warp_wait(sh.bar(BAR_Q_TMA), sc & 1, abort_flag, hdr, 52)) { ok = false; break; }
+      in_flight = false;
+    }
+    tc_fence_before();
+    warp_arrive_leader(sh.bar(BAR_Q_READY), rank);
+  }
+  // Drain (after a wait that gave up): the query copies must have landed before the CTA
+  // may exit.  Phase sc of the barrier is not over, and the next one begins here alone.
+  if (in_flight && warp == 12) mbar_wait_drain(sh.bar(BAR_Q_TMA), sc & 1);
+  __syncwarp();
+}
+
 // kTree: trees of drafted tokens (see the file's head; pages through the block table).
 template <int kMode, bool kTree>
-__global__ void __launch_bounds__(threads_of<kMode>(), 1)
+__global__ void __launch_bounds__(threads_of<kMode, kTree>(), 1)
     decode_sm103_kernel(const __grid_constant__ CUtensorMap tm_qlat, const __grid_constant__ CUtensorMap tm_qpe,
                         const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_pair,
                         const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ CUtensorMap tm_aux,
                         FastArgs a, char* ws) {
   constexpr bool kSparse = kMode == kModeSparse;
   constexpr bool kFp8 = kMode == kModeFp8;
+  constexpr bool kQueryWarps = kTree && kMode == kModeDense;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   int* hdr = reinterpret_cast<int*>(ws);
@@ -949,8 +1047,8 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
     }
     for (int i = 0; i < kPBufs; ++i) mbar_init(sh.bar(BAR_P_FULL + i), 16);
     mbar_init(sh.bar(BAR_Q_TMA), 1);
-    mbar_init(sh.bar(BAR_Q_COPIED), 8);
-    mbar_init(sh.bar(BAR_Q_READY), 16);
+    mbar_init(sh.bar(BAR_Q_COPIED), kQueryWarps ? 4 : 8);
+    mbar_init(sh.bar(BAR_Q_READY), kQueryWarps ? 8 : 16);
     mbar_init(sh.bar(BAR_Q_FREE), 1);
     mbar_init(sh.bar(BAR_O_FREE), 16);
     mbar_init(sh.bar(BAR_FINAL_QK), 1);
@@ -1048,7 +1146,7 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
         if (p0 < p1)
           asm volatile("ld.global.b32 %0, [%1];" : "=r"(blk_first) : "l"(a.block_table + (size_t)b * a.bt_stride + p0) : "memory");
         int p = p0;
-        if (sc > 0) {
+        if (!kQueryWarps && sc > 0) {
           // A later segment's first pages are requested before its query, which has to
           // wait until Q K^T is done with the previous one: at most kStages of them, so
           // that every stage they reuse held a page of an earlier segment (whose P V
@@ -1066,13 +1164,17 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
         // The first segment's whole query comes by TMA ahead of the pages (boxes 0..5
         // into ring stages 3, 4, copied to tensor memory by the softmax warps); later
         // segments' boxes 0..5 are read by those warps while the ring is in use.
-        mbar_arrive_expect_tx(sh.bar(BAR_Q_TMA), (sc == 0 ? kBoxes : kQSmemBoxes) * kQBoxBytes);
-        if (sc == 0)
-          for (int box = 0; box < kQTmemBoxes; ++box)
-            tma_load_2d(sh.q_first(box), &tm_qlat, sh.bar(BAR_Q_TMA), 64 * box, row0);
-        for (int box = kQTmemBoxes; box < 8; ++box) tma_load_2d(sh.q(box), &tm_qlat, sh.bar(BAR_Q_TMA), 64 * box, row0);
-        tma_load_2d(sh.q(8), &tm_qpe, sh.bar(BAR_Q_TMA), 0, row0);
-        q_in_flight = true;
+        // (With query warps, those take care of the later segments' queries.)
+        if (!kQueryWarps || sc == 0) {
+          mbar_arrive_expect_tx(sh.bar(BAR_Q_TMA), (sc == 0 ? kBoxes : kQSmemBoxes) * kQBoxBytes);
+          if (sc == 0)
+            for (int box = 0; box < kQTmemBoxes; ++box)
+              tma_load_2d(sh.q_first(box), &tm_qlat, sh.bar(BAR_Q_TMA), 64 * box, row0);
+          for (int box = kQTmemBoxes; box < 8; ++box)
+            tma_load_2d(sh.q(box), &tm_qlat, sh.bar(BAR_Q_TMA), 64 * box, row0);
+          tma_load_2d(sh.q(8), &tm_qpe, sh.bar(BAR_Q_TMA), 0, row0);
+          q_in_flight = true;
+        }
         for (; ok && p < p1; ++p)
           ok = load_page(b, p, p == p0 ? checked_block(a, blk_first, b, p, hdr, true) : page_block(a, b, p, hdr, true));
         ++sc;
@@ -1082,7 +1184,8 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
       for (int g = first; g < gt; ++g) {
         mbar_wait_drain(sh.bar((kFp8 ? BAR_RAW : BAR_FULL) + g % kStages), (g / kStages) & 1);
       }
-      if (q_in_flight) {
+      // (With query warps, those wait for every query's copies.)
+      if (!kQueryWarps && q_in_flight) {
         mbar_wait_drain(sh.bar(BAR_Q_TMA), (sc - 1) & 1);
       }
     } else if (lane == 1) {
@@ -1103,6 +1206,9 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
   } else if (warp == 3) {
     // idle: a warp issuing next to two softmax warps slows them (measured)
     __syncwarp();
+  } else if (kQueryWarps && warp >= 12) {
+    // ------------------------------------------------------------ the segments' queries (warps 12..15)
+    query_role(sh, smem, tmem, &tm_qlat, &tm_qpe, a, hdr, abort_flag, seg, walk0, rank, R, warp, lane);
   } else if (kFp8 && warp >= 12) {
     // ------------------------------------------------------------ FP8 row conversion (warps 12..15)
     fp8_convert_role(sh, hdr, abort_flag, seg, walk0, rank, tid - 384);
@@ -1194,7 +1300,9 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
     SegRows cur;
     if (si >= 0) {
       cur = seg_rows<kTree>(seg + (size_t)si * kSegWords, a, R, row);
-      if (!stage_q(cur, 0)) { fail(hdr, abort_flag, 33); ok = false; }
+      if constexpr (!kQueryWarps) {
+        if (!stage_q(cur, 0)) { fail(hdr, abort_flag, 33); ok = false; }
+      }
     }
     while (ok && si >= 0) {
       float m_ref = -INFINITY, l = 0.f;   // l: this thread's quarter of the row sum
@@ -1324,7 +1432,9 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
       SegRows nxt = cur;
       if (si_next >= 0) {
         nxt = seg_rows<kTree>(seg + (size_t)si_next * kSegWords, a, R, row);
-        if (!stage_q(nxt, sc + 1)) { fail(hdr, abort_flag, 33); ok = false; break; }
+        if constexpr (!kQueryWarps) {
+          if (!stage_q(nxt, sc + 1)) { fail(hdr, abort_flag, 33); ok = false; break; }
+        }
       }
       // Epilogue: wait for the last P V, combine the four quarters of the row sum,
       // then normalise and store this thread's 128 output columns.
@@ -1412,7 +1522,7 @@ __global__ void __launch_bounds__(threads_of<kMode>(), 1)
   const int num_merge = *s_num_merge;
   if (num_merge > 0) {
     const merge::Out out{a.T, a.H, a.o_lat, a.lse};
-    merge::merge_plan_share<threads_of<kMode>() / 128>(out, ws, a.L, num_merge, blockIdx.x, gridDim.x,
+    merge::merge_plan_share<threads_of<kMode, kTree>() / 128>(out, ws, a.L, num_merge, blockIdx.x, gridDim.x,
                                             reinterpret_cast<float*>(smem + kSmemRing), s_merge_ok);
   }
 }
@@ -1679,7 +1789,7 @@ cudaError_t launch_decode_sm103(const mla_geom* g, const mla_batch* b, const WsL
   if (pairs <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  cluster_launch_config(&cfg, attr, pairs, st, true, fp8 ? kFp8Threads : kThreads);
+  cluster_launch_config(&cfg, attr, pairs, st, true, fp8 ? kFp8Threads : tree ? kQueryThreads : kThreads);
   char* w = reinterpret_cast<char*>(ws);
   auto launch = [&](auto kernel) {
     return cudaLaunchKernelEx(&cfg, kernel, m_qlat, m_qpe, m_page, m_pair, m_kpe, m_aux, a, w);

@@ -262,3 +262,24 @@ def test_captured_and_replayed_with_new_lengths(mla, cuda):
     torch.cuda.synchronize()
     assert mla.mla_read_device_status(t.ws)[0] == mla.MLA_OK
     t.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_timeouts_are_reported_and_recoverable(mla, cuda, fp8):
+    """Pipeline waits shortened to a few cycles (nothing faults): the launch reports and the next one is right."""
+    import torch
+    t = Tree(mla, torch, cuda, 128, [1024, 1000, 1024, 990], 3, fp8=fp8, sharp=not fp8, slots=12, ahead=False)
+    t.plan()
+    torch.cuda.synchronize()
+    assert int(t.ws[:256].view(torch.int32)[mla.HDR["NUM_MERGE"]]) == 0
+    try:
+        mla.check(mla.mla_debug_set_wait_limit(16), "set wait limit")
+        for _ in range(2):
+            t.plan()
+            t.decode(checked=0)
+            torch.cuda.synchronize()
+            status, info = mla.mla_read_device_status(t.ws)
+            assert status == mla.MLA_ERR_TIMEOUT and info > 0
+    finally:
+        mla.check(mla.mla_debug_set_wait_limit(0), "reset wait limit")
+    t.run().check()
