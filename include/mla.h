@@ -261,8 +261,9 @@ mla_status mla_decode_sparse(const mla_geom* geom, const mla_batch* batch, const
  *   A query token that sees nothing, and every t >= n_b, gets o_lat = 0 and lse = -inf.
  *   The rows before the nodes', and each node's row that some node of its sequence
  *   sees, hold finite values; what other rows hold (NaN too) does not matter.
- * mla_plan_tree stands in for mla_plan (the same workspace and size), and is re-run
- * when the lengths or node counts change; the mask is the decode's alone.  checked, the
+ * mla_plan_tree stands in for mla_plan (the same workspace, size and split rule, but
+ * for ranges of at least 2 pages in place of 4; groups past a sequence's nodes need no
+ * page), and is re-run when the lengths or node counts change; the mask is the decode's alone.  checked, the
  * status word and every other argument as for mla_decode and mla_decode_fp8.
  * mla_decode_tree_fp8 given mla_tree_fp8_workspace_size() bytes (0 on invalid
  * arguments; as much as the batch's longest table as bf16 rows on top of the plan's)

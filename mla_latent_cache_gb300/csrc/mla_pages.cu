@@ -62,24 +62,36 @@ __device__ int block_excl_scan(int v, int* total, int* sh) {
   return pre + x - v;
 }
 
+// This thread's refs entries of the scan step that starts at block `base`.
+struct RefsChunk {
+  int v[kScanPerThread];
+};
+__device__ __forceinline__ RefsChunk load_refs(const int32_t* refs, int num_blocks, int base) {
+  const int k0 = base + threadIdx.x * kScanPerThread;
+  RefsChunk c;
+#pragma unroll
+  for (int g = 0; g < kScanPerThread; g += 4) {
+    if (k0 + g + 4 <= num_blocks) {
+      const int4 u = __ldcg(reinterpret_cast<const int4*>(refs + k0 + g));
+      c.v[g] = u.x; c.v[g + 1] = u.y; c.v[g + 2] = u.z; c.v[g + 3] = u.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c.v[g + e] = k0 + g + e < num_blocks ? __ldcg(refs + k0 + g + e) : 1;
+    }
+  }
+  return c;
+}
+
 // take(rank, block) for the `want` lowest free blocks, ranks 0 .. in block order; returns
-// how many there were.  refs entries taken here are written by `take` itself.
+// how many there were.  chunk: the entries from block 0 on, loaded by the caller.  refs
+// entries taken here are written by `take` itself.
 template <typename Take>
-__device__ int take_free(const int32_t* refs, int num_blocks, int want, int* sh, Take take) {
+__device__ int take_free(const int32_t* refs, int num_blocks, int want, int* sh, RefsChunk chunk, Take take) {
   int found = 0;
   for (int base = 0; base < num_blocks && found < want; base += kBookThreads * kScanPerThread) {
     const int k0 = base + threadIdx.x * kScanPerThread;
-    int v[kScanPerThread];
-#pragma unroll
-    for (int g = 0; g < kScanPerThread; g += 4) {
-      if (k0 + g + 4 <= num_blocks) {
-        const int4 u = __ldcg(reinterpret_cast<const int4*>(refs + k0 + g));
-        v[g] = u.x; v[g + 1] = u.y; v[g + 2] = u.z; v[g + 3] = u.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[g + e] = k0 + g + e < num_blocks ? __ldcg(refs + k0 + g + e) : 1;
-      }
-    }
+    if (base > 0) chunk = load_refs(refs, num_blocks, base);
+    const int (&v)[kScanPerThread] = chunk.v;
     int mine = 0;
 #pragma unroll
     for (int g = 0; g < kScanPerThread; ++g) mine += v[g] == 0;
@@ -118,12 +130,14 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CompactArgs a) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x, tid = threadIdx.x;
+  const int32_t* idx = a.accept_idx + (size_t)b * a.T;
+  // (a thread's first node is asked for together with the lengths)
+  const int t_first = tid < a.T ? idx[tid] : 0, prev_first = tid > 0 && tid < a.T ? idx[tid - 1] : -1;
   const int S = a.seq_lens[b], n = a.node_lens ? a.node_lens[b] : a.T, acc = a.accept_len[b];
   bool bad = n < 0 || n > a.T || S < n || S > a.max_pages * kPage || acc < 0 || acc > n;
   if (!bad) {
-    const int32_t* idx = a.accept_idx + (size_t)b * a.T;
     for (int i = tid; i < acc; i += kCopyThreads) {
-      const int t = idx[i], prev = i ? idx[i - 1] : -1;
+      const int t = i == tid ? t_first : idx[i], prev = i == tid ? prev_first : idx[i - 1];
       if (t <= prev || t >= n) { bad = true; continue; }
       const int from = S - n + t, to = S - n + i;
       const int bf = a.block_table[(size_t)b * a.bt_stride + from / kPage];
@@ -171,26 +185,53 @@ struct ResizeArgs {
   int* status;
 };
 
+// The last index of the non-decreasing v[0 .. n) with v[index] <= x (v[0] <= x).
+__device__ __forceinline__ int last_at_most(const int* v, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
 __device__ __forceinline__ int pages_of(int len) { return (int)(((long long)len + kPage - 1) / kPage); }
 
 __global__ void __launch_bounds__(kBookThreads) resize_kernel(ResizeArgs a) {
   extern __shared__ int first[];       // [B]: pages asked for by the sequences before b
-  __shared__ int sh[33];
+  __shared__ int sh[33], back_first[kBookThreads], back_page[kBookThreads];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int max_rows = a.max_pages * kPage;
-  // Releases first: a warp per sequence, a lane per page.
-  for (int b = warp; b < a.B; b += kBookThreads / 32) {
-    const int cur = a.cur_lens[b], len = a.new_lens[b];
-    if (cur < 0 || cur > max_rows || len < 0 || len > max_rows) {
-      if (lane == 0) report(a.status);
-      continue;
+  // For 1024 sequences at a time: the pages to give back and those asked for, counted and
+  // ranked in sequence order; then the former, one page per thread.
+  int want = 0;
+  for (int base = 0; base < a.B; base += kBookThreads) {
+    const int b = base + tid;
+    int need = 0, back = 0, keep = 0;
+    if (b < a.B) {
+      const int cur = a.cur_lens[b], len = a.new_lens[b];
+      if (cur < 0 || cur > max_rows || len < 0 || len > max_rows) {
+        report(a.status);
+      } else {
+        keep = pages_of(len);
+        need = max(0, keep - pages_of(cur));
+        back = max(0, pages_of(cur) - keep);
+      }
     }
-    int32_t* row = a.block_table + (size_t)b * a.bt_stride;
-    for (int p = pages_of(len) + lane; p < pages_of(cur); p += 32) {
-      const int k = row[p];
-      row[p] = -1;
+    int total_need, total_back;
+    const int pre_need = block_excl_scan(need, &total_need, sh);
+    const int pre_back = block_excl_scan(back, &total_back, sh);
+    if (b < a.B) first[b] = want + pre_need;
+    want += total_need;
+    back_first[tid] = pre_back;
+    back_page[tid] = keep;
+    __syncthreads();
+    for (int i = tid; i < total_back; i += kBookThreads) {
+      const int j = last_at_most(back_first, kBookThreads, i);
+      int32_t* entry = a.block_table + (size_t)(base + j) * a.bt_stride + back_page[j] + (i - back_first[j]);
+      const int k = *entry;
+      *entry = -1;
       if (k < 0 || k >= a.num_blocks) {
         report(a.status);
       } else if (atomicSub(&a.refs[k], 1) <= 0) {   // held by nobody: the count stays at 0
@@ -198,30 +239,13 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(ResizeArgs a) {
         report(a.status);
       }
     }
+    __syncthreads();
   }
   __threadfence();
   __syncthreads();
-  // Pages asked for, in sequence order.
-  int want = 0;
-  for (int base = 0; base < a.B; base += kBookThreads) {
-    const int b = base + tid;
-    int need = 0;
-    if (b < a.B) {
-      const int cur = a.cur_lens[b], len = a.new_lens[b];
-      if (cur >= 0 && cur <= max_rows && len >= 0 && len <= max_rows) need = max(0, pages_of(len) - pages_of(cur));
-    }
-    int total;
-    const int pre = block_excl_scan(need, &total, sh);
-    if (b < a.B) first[b] = want + pre;
-    want += total;
-  }
-  __syncthreads();
-  const int got = want == 0 ? 0 : take_free(a.refs, a.num_blocks, want, sh, [&](int rank, int k) {
-    int lo = 0, hi = a.B;              // the last sequence whose first page's rank is <= rank
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= rank) lo = mid; else hi = mid;
-    }
+  const RefsChunk chunk = want == 0 ? RefsChunk{} : load_refs(a.refs, a.num_blocks, 0);
+  const int got = want == 0 ? 0 : take_free(a.refs, a.num_blocks, want, sh, chunk, [&](int rank, int k) {
+    const int lo = last_at_most(first, a.B, rank);
     a.block_table[(size_t)lo * a.bt_stride + pages_of(a.cur_lens[lo]) + rank - first[lo]] = k;
     a.refs[k] = 1;
   });
@@ -270,6 +294,9 @@ __global__ void __launch_bounds__(kBookThreads) fork_plan_kernel(ForkArgs a) {
   int* fork_of = dyn;
   unsigned* once = reinterpret_cast<unsigned*>(dyn + a.F);
   unsigned* twice = once + words;
+  // (the scan's first blocks are on their way while the forks are looked at: no fork's
+  // decision writes a count)
+  const RefsChunk chunk = load_refs(a.refs, a.num_blocks, 0);
   for (int w = tid; w < 2 * words; w += kBookThreads) once[w] = 0;
   __syncthreads();
   for (int f = tid; f < a.F; f += kBookThreads) {
@@ -320,7 +347,7 @@ __global__ void __launch_bounds__(kBookThreads) fork_plan_kernel(ForkArgs a) {
     want += total;
   }
   __syncthreads();
-  const int got = want == 0 ? 0 : take_free(a.refs, a.num_blocks, want, sh, [&](int rank, int k) {
+  const int got = want == 0 ? 0 : take_free(a.refs, a.num_blocks, want, sh, chunk, [&](int rank, int k) {
     a.copies[a.F + fork_of[rank]] = k;
     a.refs[k] = 1;
   });

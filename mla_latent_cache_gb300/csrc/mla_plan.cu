@@ -10,6 +10,16 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
+// Trees: the least pages of a range.  A range's first page is in its pair's hands after
+// ~6 us whatever its length, and every further one takes ~0.9 us, against the merge of
+// more parts (one tree of 8 nodes x 16 heads over 512 rows, decode: 4 pages 16.0 us, 2
+// pages 14.4, 1 page 13.6; 4 nodes x 128 heads over 850 rows, plan and decode: 21.9, 20.9,
+// 21.9).
+constexpr int kTreeMinSplitPages = 2;
+// Trees: threads of the planner.  Up to this many groups one per thread, few enough for
+// cheap barriers (one group 4.0 us with 256 threads, 4.9 with 1024; 512 groups 9.9, 8.4).
+constexpr int kTreePlanThreads = 256;
+
 constexpr int kSmemGroups = 4096;   // groups whose segment bases the planner keeps in shared memory
 
 // Block-wide exclusive scans of three ints per thread at once; tot[] gets the
@@ -202,7 +212,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
   const int W = carry;
   if (tid == 0) {
     int q = (W + a.G - 1) / a.G;
-    q = q < kMinSplitPages ? kMinSplitPages : q;
+    const int least = a.tree ? kTreeMinSplitPages : kMinSplitPages;
+    q = q < least ? least : q;
     s_q = q;
     if (a.N > 0) s_mode = 2;
     else if (nonempty <= a.G && maxn <= (5 * q + 3) / 4) s_mode = 0;
@@ -211,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
       // balanced ranges over the line of pages and gaps
       const int U = W + kSegmentCostPages * (nonempty - 1);
       const int qw = (U + a.G - 1) / a.G;
-      s_q = qw < kMinSplitPages ? kMinSplitPages : qw;
+      s_q = qw < least ? least : qw;
       s_U = U;
     }
   }
@@ -327,7 +338,8 @@ cudaError_t launch_plan(const int32_t* seq_lens, const mla_geom* g, const mla_ba
   a.tree = tree != nullptr;
   a.node_lens = tree ? tree->node_lens : nullptr;
   a.L = L;
-  return launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a, reinterpret_cast<char*>(ws));
+  const int threads = tree && a.num_groups <= kTreePlanThreads ? kTreePlanThreads : kPlanThreads;
+  return launch_pdl(plan_kernel, dim3(1), dim3(threads), 0, st, a, reinterpret_cast<char*>(ws));
 }
 
 }  // namespace mla
