@@ -138,9 +138,10 @@ def lib() -> ctypes.CDLL:
 def _ptr(t) -> int | None:
     if t is None:
         return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:      # an address
         return t
-    return t.data_ptr()
 
 
 def _torch_stream() -> int:
