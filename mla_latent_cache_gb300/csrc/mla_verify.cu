@@ -17,12 +17,11 @@
 //
 // The draw: the first x, in vocabulary order, with R(0) + ... + R(x) > u_sample * Z.
 //
-// Decisions lie next to borders, so sums are kept to about 1e-13 of the mass: the
-// inputs are fp32 or bf16 (u q(x) and the widened values are exact in fp64), the walk's
-// scalars are fp64, and a row is summed by each lane in pairs of fp32 (a value and what
-// its rounding lost; every difference p - C q and every addition keeps its error term),
-// joined in fp64.  The fp64 pipe does two operations per cycle and SM here: a row of
-// fp64 additions took 286 us for 64 sequences of 129280 entries, where reading takes 10.
+// Decisions lie next to borders, so every sum, product and comparison is done in pairs of
+// fp32 (a value and what its rounding lost, Dekker's and Knuth's error-free sums and
+// products): sums are good to about 1e-13 of the mass, and u q(x) is exact.  fp64 itself
+// is too slow here, at two operations per cycle and SM: 64 sequences of 129280 entries took
+// 286 us with rows summed in fp64, where reading them takes 10.
 //
 // Bound by memory: of T rows only those at which a draft is refused are read, p and q
 // once each, and once more the sixteenth of a slice that holds the drawn token.  A
@@ -85,36 +84,52 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* row, int x, int V, fl
   }
 }
 
-// What is left of p: p - C q, or p without the refused tokens.
-struct Residual {
-  double C;                  // > 0: subtract C q
-  int num_refused;           // > 0: these tokens are out (point-mass drafts)
-  const int* refused;
-  const uint32_t* filter;
-};
-
 // An unevaluated sum of two fp32 values, hi the sum rounded.
 struct Pair {
   float hi, lo;
 };
-__device__ __forceinline__ Pair two_diff(float a, float b) {     // a - b, exactly
-  const float d = a - b, t = d - a;
-  return {d, (a - (d - t)) - (b + t)};
+__device__ __forceinline__ Pair two_sum(float a, float b) {      // a + b, exactly
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
 }
-__device__ __forceinline__ void add_to(Pair& s, Pair v) {
-  const float t = s.hi + v.hi, b = t - s.hi;
-  s.lo += ((s.hi - (t - b)) + (v.hi - b)) + v.lo;
-  s.hi = t;
+__device__ __forceinline__ Pair quick_sum(float a, float b) {    // the same for |a| >= |b|
+  const float s = a + b;
+  return {s, b - (s - a)};
 }
-__device__ __forceinline__ Pair shfl_xor(Pair v, int o) {
-  return {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)};
+__device__ __forceinline__ Pair two_prod(float a, float b) {     // a b, exactly
+  const float p = a * b;
+  return {p, fmaf(a, b, -p)};
 }
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__device__ __forceinline__ void add_to(Pair& s, Pair v) {        // lo not carried into hi
+  const Pair t = two_sum(s.hi, v.hi);
+  s.lo += t.lo + v.lo;
+  s.hi = t.hi;
 }
-__device__ __forceinline__ double value(Pair v) { return (double)v.hi + (double)v.lo; }
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair s = two_sum(a.hi, b.hi);
+  const Pair t = two_sum(a.lo, b.lo);
+  s = quick_sum(s.hi, s.lo + t.hi);
+  return quick_sum(s.hi, s.lo + t.lo);
+}
+__device__ __forceinline__ Pair sub(Pair a, Pair b) { return add(a, {-b.hi, -b.lo}); }
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const Pair p = two_prod(a.hi, b.hi);
+  return quick_sum(p.hi, p.lo + fmaf(a.hi, b.lo, a.lo * b.hi));
+}
+__device__ __forceinline__ Pair scaled(Pair a, float power_of_2) { return {a.hi * power_of_2, a.lo * power_of_2}; }
+__device__ __forceinline__ bool less(Pair a, Pair b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+
+// Masses, and what is compared with them, are held times 2^64: products with a number
+// u >= 2^-24 and their error terms then stay in fp32's range for masses down to its least.
+constexpr float kScale = 18446744073709551616.f, kUnscale = 1.f / kScale;
+
+// What is left of p: p - C q, or p without the refused tokens.
+struct Residual {
+  Pair C;                    // > 0: subtract C q
+  int num_refused;           // > 0: these tokens are out (point-mass drafts)
+  const int* refused;
+  const uint32_t* filter;
+};
 
 // Entries [x, x + 8) of what is left.
 template <typename T>
@@ -122,20 +137,18 @@ __device__ __forceinline__ void residual8(const T* p_row, const T* q_row, const 
                                           Pair (&out)[8]) {
   float p[8];
   load8(p_row, x, V, p);
-  if (r.C > 0.0) {
+  if (r.C.hi > 0.f) {
     float q[8];
     load8(q_row, x, V, q);
-    if (r.C == 1.0) {
+    if (r.C.hi == 1.f && r.C.lo == 0.f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] = two_diff(clean(p[e]), clean(q[e]));
+      for (int e = 0; e < 8; ++e) out[e] = two_sum(clean(p[e]), -clean(q[e]));
     } else {
-      const float ch = (float)r.C, cl = (float)(r.C - (double)ch);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float qe = clean(q[e]), h = ch * qe, l = fmaf(cl, qe, fmaf(ch, qe, -h));
-        const Pair d = two_diff(clean(p[e]), h);
-        const float lo = d.lo - l, hi = d.hi + lo;
-        out[e] = {hi, lo - (hi - d.hi)};
+        const float qe = clean(q[e]);
+        const Pair cq = two_prod(r.C.hi, qe), d = two_sum(clean(p[e]), -cq.hi);
+        out[e] = quick_sum(d.hi, d.lo - fmaf(r.C.lo, qe, cq.lo));
       }
     }
 #pragma unroll
@@ -165,9 +178,40 @@ __device__ __forceinline__ void part_of(int t0, int t1, int k, int n, int* first
   *last = t0 + (int)(len * (k + 1) / n);
 }
 
-// The masses of the warps' parts of the tiles [t0, t1) into wsum[] (the whole CTA).
+__device__ __forceinline__ Pair shfl(Pair v, int lane) {
+  return {__shfl_sync(0xffffffffu, v.hi, lane), __shfl_sync(0xffffffffu, v.lo, lane)};
+}
+// (Called behind a branch that some lanes take, a warp goes through these in two parts that
+// meet at every shuffle: 3300 cycles in place of 550, measured.  So what their callers pass
+// is chosen by selects, find_part adds zeros where a lane has nothing to add, and one
+// lane's stores are followed by __syncwarp.)
+__device__ __forceinline__ Pair keep_if(bool keep, Pair v) { return {keep ? v.hi : 0.f, keep ? v.lo : 0.f}; }
+__device__ __noinline__ Pair warp_sum(Pair v) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1)
+    v = add(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
+// What is left of entry x alone (x < V).
 template <typename T>
-__device__ void part_masses(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1, Pair* wsum) {
+__device__ __forceinline__ Pair residual1(const T* p_row, const T* q_row, const Residual& r, int x) {
+  Pair v{clean(widen(p_row[x])), 0.f};
+  if (r.C.hi > 0.f) {
+    const Pair cq = mul(r.C, {clean(widen(q_row[x])), 0.f});
+    v = sub(v, cq);
+    if (!(v.hi > 0.f)) v = {0.f, 0.f};
+  }
+  for (int k = 0; k < r.num_refused; ++k)
+    if (r.refused[k] == x) v = {0.f, 0.f};
+  return v;
+}
+
+// The masses (scaled) of the warps' parts of the tiles [t0, t1) into wsum[], of their lanes
+// into lsum[] (the whole CTA).
+template <typename T>
+__device__ __noinline__ void part_masses(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1,
+                                         Pair* wsum, Pair* lsum) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int first, last;
   part_of(t0, t1, w, kVerifyWarps, &first, &last);
@@ -179,78 +223,47 @@ __device__ void part_masses(const T* p_row, const T* q_row, const Residual& r, i
 #pragma unroll
     for (int e = 0; e < 8; ++e) add_to(s, v[e]);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) add_to(s, shfl_xor(s, o));
-  __syncthreads();   // wsum's last readers are done
-  if (lane == 0) wsum[w] = s;
+  s = scaled(quick_sum(s.hi, s.lo), kScale);
+  const Pair all = warp_sum(s);
+  __syncthreads();   // the last readers of wsum and lsum are done
+  lsum[threadIdx.x] = s;
+  if (lane == 0) wsum[w] = all;
   __syncthreads();
 }
 
 // One warp, lane k holding the mass m of part k (0 past the last): the part that holds
 // the entry at which the running sum, `run` at first, passes `goal`; the last part with
-// mass if rounding leaves none (-1: no mass).  run becomes the sum before that part.
-__device__ __forceinline__ int find_part(double m, double* run, double goal) {
+// mass if rounding leaves none (-1: no mass).  And the sum before that part.
+struct Found {
+  int part;
+  Pair run;
+};
+__device__ __noinline__ Found find_part(Pair m, Pair run, Pair goal) {
   const int lane = threadIdx.x & 31;
-  double incl = m;
-#pragma unroll
+  Pair incl = m;
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const Pair y{__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
+    incl = add(incl, keep_if(lane >= o, y));
   }
-  const unsigned some = __ballot_sync(0xffffffffu, m > 0.0);
-  const unsigned hit = __ballot_sync(0xffffffffu, m > 0.0 && *run + incl > goal);
+  incl = add(run, incl);
+  const unsigned some = __ballot_sync(0xffffffffu, m.hi > 0.f);
+  const unsigned hit = __ballot_sync(0xffffffffu, m.hi > 0.f && less(goal, incl));
   const int k = hit ? __ffs(hit) - 1 : 31 - __clz(some);
-  if (k >= 0) *run += __shfl_sync(0xffffffffu, incl - m, k);
-  return k;
-}
-
-// One warp: the first entry of the tiles [t0, t1) whose running sum, from `run` on,
-// passes `goal`; their last entry of positive mass if rounding leaves none.
-template <typename T>
-__device__ int warp_find(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1, double run,
-                         double goal) {
-  const int lane = threadIdx.x & 31;
-  int last = -1;
-  for (int t = t0; t < t1; ++t) {
-    Pair v[8], s{0.f, 0.f};
-    residual8(p_row, q_row, r, t * kTile + 8 * lane, V, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      add_to(s, v[e]);
-      if (v[e].hi > 0.f) last = t * kTile + 8 * lane + e;
-    }
-    double before = run;
-    const double mine = value(s);
-    int src = find_part(mine, &before, goal);
-    // the lane found passes the goal, or is the last one with mass of a tile that does not
-    const double after = before + __shfl_sync(0xffffffffu, mine, src < 0 ? 0 : src);
-    if (src >= 0 && after > goal) {
-      // its eight entries, one per lane
-      Pair e8{0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const Pair x{__shfl_sync(0xffffffffu, v[e].hi, src), __shfl_sync(0xffffffffu, v[e].lo, src)};
-        if (lane == e) e8 = x;
-      }
-      return t * kTile + 8 * src + find_part(value(e8), &before, goal);
-    }
-    if (src >= 0) run = after;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
-  return last;
+  const Pair before = shfl(incl, k > 0 ? k - 1 : 0);
+  return {k, k > 0 ? before : run};
 }
 
 // What the walking warp tells the others.
 struct Walk {
   int cur, count, nref, want_mass;
-  double C;
+  Pair C;
 };
 
-// What warp 0 decides about the draw: the CTA (-1: nothing is left) and its warp's part.
+// What warp 0 decides about the draw: the CTA (-1: nothing is left), and the tiles that
+// hold the token.
 struct Draw {
-  int cta, part;
-  double run, goal;
+  int cta, t0, t1;
 };
 
 // One cluster of CTAs per sequence.
@@ -258,16 +271,18 @@ template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a) {
   extern __shared__ int smem[];      // tokens, parents, p(x), q(x), u per node; the path; refused tokens
   __shared__ Pair wsum[kVerifyWarps];
-  __shared__ double slice[2][kMaxCluster];   // the CTAs' masses, by turns
+  __shared__ float2 slice[2][kMaxCluster];   // the CTAs' masses, by turns
   __shared__ uint32_t filter[kFilterBits / 32];
   __shared__ Walk s_walk;
+  __shared__ Pair lsum[kVerifyThreads];
   __shared__ int s_next;
   __shared__ Draw s_draw;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   ptx::cluster_sync_all();   // the other CTAs run: their shared memory may be written
   pdl_wait();
   pdl_trigger();
   const int rank = (int)ptx::cluster_ctarank(), size = a.cluster;
-  const int b = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / size;
   const int N = a.T;
   int* tok = smem;
   int* par = smem + N;
@@ -277,6 +292,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
   int* path = smem + 5 * N;
   int* refused = smem + 6 * N;
   int n = a.node_lens ? a.node_lens[b] : N;
+  const float us = a.u_sample[b];
   bool bad = n < 0 || n > N;
   if (bad) n = 0;
   const T* target = static_cast<const T*>(a.target) + (size_t)b * N * a.row_stride;
@@ -298,33 +314,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
 
   int t0, t1, turn = 0;
   part_of(0, (a.V + kTile - 1) / kTile, rank, size, &t0, &t1);
-  // The mass of what is left of a row: lane k of warp 0 gets the mass of CTA k's slice
-  // (fp64 from here on is one warp's: an instruction takes its pipe for 16 cycles).
-  auto mass = [&](const T* p_row, const T* q_row, const Residual& r) -> double {
-    part_masses(p_row, q_row, r, a.V, t0, t1, wsum);
-    if (warp == 0) {
-      const double mine = warp_sum(lane < kVerifyWarps ? value(wsum[lane]) : 0.0);
-      if (lane < size) {
-        const uint32_t to = ptx::map_to_cta(ptx::smem_addr(&slice[turn][rank]), lane);
-        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(mine) : "memory");
-      }
-    }
-    __syncwarp();
-    ptx::cluster_sync_all();
-    const double m = warp == 0 && lane < size ? slice[turn][lane] : 0.0;
-    turn ^= 1;
-    return m;
-  };
+  const T *p_row = target, *q_row = draft;
+  Residual r;
 
-  // The walk (warp 0), stopping where a refusal asks for the mass left.
-  int cur = 0, at = 0, count = n > 0 ? 1 : 0, nref = 0;
-  double C = 0.0, Z = 1.0;
+  // The walk (warp 0), stopping where a refusal asks for the mass left; at its end the draw.
+  int cur = 0, at = 0, count = 1, nref = 0;
+  const Pair none{0.f, 0.f}, one{kScale, 0.f};
+  Pair C = none, Z = one, run = none, goal = none;   // Z scaled
   bool stale = false;     // Z has to be summed anew
-  if (tid == 0 && n > 0) path[0] = 0;
-  while (true) {
-    if (warp == 0) {
+  bool bare = false;      // the draw is from p itself
+  if (tid == 0) path[0] = 0;
+  while (n > 0) {
+    if (warp == 0 && !bare) {
       int want = 0;
-      while (n > 0) {
+      while (true) {
         // the next child of cur, in index order
         int child = -1;
         for (int base = at + 1; base < n; base += 32) {
@@ -334,96 +337,120 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
         if (child < 0) break;
         if (stale) { want = 1; break; }
         at = child;
-        const double u = (double)ua[child], p = (double)px[child], q = (double)qx[child];
-        double left = p - C * q;
-        if (!draft) {
+        const float u = ua[child], p = px[child], q = qx[child];
+        Pair left{p, 0.f};
+        if (draft) {
+          if (C.hi > 0.f) left = sub(left, mul(C, {q, 0.f}));
+        } else {
           bool again = false;
           for (int base = 0; base < nref; base += 32)
             again |= __any_sync(0xffffffffu, base + lane < nref && refused[base + lane] == tok[child]);
-          left = again ? 0.0 : p;
+          if (again) left = none;
         }
-        if (left > 0.0 && u * q * Z < left) {
+        left = scaled(left, kScale);
+        const float half = 4294967296.f;   // sqrt(kScale), shared by the two products
+        if (left.hi > 0.f && less(mul(two_prod(u * half, q), scaled(Z, 1.f / half)), left)) {
           cur = child;
           if (lane == 0) path[count] = child;
+          __syncwarp();
           ++count;
-          C = 0.0; Z = 1.0; nref = 0;
+          C = none; Z = one; nref = 0;
         } else if (draft) {
-          C += Z;
+          C = add(C, scaled(Z, kUnscale));
           stale = true;
         } else {
-          if (left > 0.0) Z -= left;
+          if (left.hi > 0.f) Z = sub(Z, left);
           if (lane == 0) refused[nref] = tok[child];
           ++nref;
           __syncwarp();
         }
       }
+      for (int k = lane; k < nref; k += 32) {     // (at the walk's end only: nobody looks before)
+        const int bit = (refused[k] >> 3) & (kFilterBits - 1);
+        if (!want) atomicOr(&filter[bit >> 5], 1u << (bit & 31));
+      }
+      __syncwarp();
       if (lane == 0) s_walk = Walk{cur, count, nref, want, C};
     }
     __syncthreads();
     const Walk w = s_walk;
-    if (!w.want_mass) break;
-    const Residual r{w.C, 0, nullptr, filter};
-    const double m = mass(target + (size_t)w.cur * a.row_stride, draft + (size_t)w.cur * a.row_stride, r);
+    p_row = target + (size_t)w.cur * a.row_stride;
+    q_row = draft ? draft + (size_t)w.cur * a.row_stride : nullptr;
+    r = Residual{bare ? none : w.C, bare || w.want_mass ? 0 : w.nref, refused, filter};
+    // The mass (scaled) of what is left of the row: lane k of warp 0 gets that of CTA k's slice.
+    part_masses(p_row, q_row, r, a.V, t0, t1, wsum, lsum);
     if (warp == 0) {
-      Z = warp_sum(m);
-      stale = false;
+      const Pair mine = warp_sum(keep_if(lane < kVerifyWarps, wsum[lane % kVerifyWarps]));
+      if (lane < size) {
+        const uint32_t to = ptx::map_to_cta(ptx::smem_addr(&slice[turn][rank]), lane);
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(mine.hi), "f"(mine.lo) : "memory");
+      }
     }
+    __syncwarp();
+    ptx::cluster_sync_all();
+    if (warp == 0) {
+      const float2 s = slice[turn][lane % kMaxCluster];
+      const Pair m = keep_if(lane < size, {s.x, s.y});
+      const Pair total = warp_sum(m);
+      Z = total;
+      stale = false;
+      // the draw: the CTA whose slice holds the token, if this was the walk's end
+      int cta = -1;
+      goal = mul(total, {us, 0.f});
+      if (total.hi > 0.f && !w.want_mass) {
+        const Found f = find_part(m, none, goal);
+        cta = f.part;
+        run = f.run;
+      }
+      if (lane == 0) s_draw = Draw{cta, t0, t1};
+    }
+    turn ^= 1;
+    __syncthreads();
+    if (w.want_mass) continue;
+    if (s_draw.cta >= 0 || bare) break;
+    bare = true;          // nothing is left: p lies under the drafts everywhere
   }
 
-  const Walk w = s_walk;
   int next = -1, writer = 0;
+  const int count_all = n > 0 ? s_walk.count : 0;
   if (n > 0) {
-    for (int k = tid; k < w.nref; k += kVerifyThreads) {
-      const int bit = (refused[k] >> 3) & (kFilterBits - 1);
-      atomicOr(&filter[bit >> 5], 1u << (bit & 31));
-    }
-    __syncthreads();
-    const T* p_row = target + (size_t)w.cur * a.row_stride;
-    const T* q_row = draft ? draft + (size_t)w.cur * a.row_stride : nullptr;
-    Residual r{w.C, w.nref, refused, filter};
-    // Warp 0 decides: the CTA whose slice holds the drawn token, and the part of it.
-    auto decide = [&](double m) {
-      if (warp == 0) {
-        const double total = warp_sum(m);
-        Draw d{-1, -1, 0.0, (double)a.u_sample[b] * total};
-        if (total > 0.0) {
-          d.cta = find_part(m, &d.run, d.goal);
-          if (d.cta == rank) d.part = find_part(lane < kVerifyWarps ? value(wsum[lane]) : 0.0, &d.run, d.goal);
-        }
-        if (lane == 0) s_draw = d;
-      }
-      __syncthreads();
-    };
-    decide(mass(p_row, q_row, r));
-    if (s_draw.cta < 0 && (r.C > 0.0 || r.num_refused > 0)) {
-      // nothing is left (p lies under the drafts everywhere): the draw is from p itself
-      r.C = 0.0;
-      r.num_refused = 0;
-      const double m = mass(p_row, q_row, r);
-      decide(m);
-    }
     if (s_draw.cta >= 0) writer = s_draw.cta;
     if (s_draw.cta == rank) {
-      part_of(t0, t1, s_draw.part, kVerifyWarps, &t0, &t1);
-      part_masses(p_row, q_row, r, a.V, t0, t1, wsum);       // that part shared out again, and the token in it
-      if (warp == 0) {
-        double run = s_draw.run;
-        const double goal = s_draw.goal;
-        const int k = find_part(lane < kVerifyWarps ? value(wsum[lane]) : 0.0, &run, goal);
-        part_of(t0, t1, k, kVerifyWarps, &t0, &t1);
-        const int x = warp_find(p_row, q_row, r, a.V, t0, t1, run, goal);
-        if (lane == 0) s_next = x;
+      // The part of the tiles that holds the token, shared out again until each warp has one
+      // tile at most; then its warp's lane, and that lane's entry.
+      while (true) {
+        const int first = s_draw.t0, last = s_draw.t1;
+        __syncthreads();
+        if (warp == 0) {
+          const Found w = find_part(keep_if(lane < kVerifyWarps, wsum[lane % kVerifyWarps]), run, goal);
+          const int k = max(0, w.part);
+          run = w.run;
+          int f, l;
+          part_of(first, last, k, kVerifyWarps, &f, &l);
+          if (last - first <= kVerifyWarps) {
+            const Found in_tile = find_part(lsum[32 * k + lane], run, goal);
+            const int x = f * kTile + 8 * max(0, in_tile.part);
+            // (a lane past the tile's eight, or the vocabulary, looks at the last entry for nothing)
+            const int mine = min(x + min(lane, 7), a.V - 1);
+            const Pair e = keep_if(mine == x + lane, scaled(residual1(p_row, q_row, r, mine), kScale));
+            const Found entry = find_part(e, in_tile.run, goal);
+            if (lane == 0) s_next = x + max(0, entry.part);
+          }
+          if (lane == 0) s_draw = Draw{rank, f, l};
+        }
+        __syncthreads();
+        if (last - first <= kVerifyWarps) break;
+        part_masses(p_row, q_row, r, a.V, s_draw.t0, s_draw.t1, wsum, lsum);
       }
-      __syncthreads();
       next = s_next;
     }
   }
   if (rank != writer) return;
   for (int t = tid; t < N; t += kVerifyThreads) {
-    a.accept_idx[(size_t)b * N + t] = t < w.count ? path[t] : -1;
-    a.out_tokens[(size_t)b * N + t] = t + 1 < w.count ? tok[path[t + 1]] : (t + 1 == w.count ? next : -1);
+    a.accept_idx[(size_t)b * N + t] = t < count_all ? path[t] : -1;
+    a.out_tokens[(size_t)b * N + t] = t + 1 < count_all ? tok[path[t + 1]] : (t + 1 == count_all ? next : -1);
   }
-  if (tid == 0) a.accept_len[b] = w.count;
+  if (tid == 0) a.accept_len[b] = count_all;
 }
 
 }  // namespace
