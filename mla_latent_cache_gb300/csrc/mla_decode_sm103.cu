@@ -324,8 +324,8 @@ __device__ __forceinline__ uint32_t tree_bits(const FastArgs& a, const SegRows& 
   if (count <= 0) return 0;
   const uint32_t* m = a.tree_mask + ((size_t)s.b * a.T + s.fr / a.H) * a.tree_words;
   const int w = u0 >> 5;                     // -1 for a negative u0 (u0 >= -15 where this is called)
-  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : __ldg(m + w);
-  const uint32_t hi = w + 1 < a.tree_words ? __ldg(m + w + 1) : 0u;
+  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : m[w];
+  const uint32_t hi = w + 1 < a.tree_words ? m[w + 1] : 0u;
   const uint32_t bits = __funnelshift_r(lo, hi, u0 & 31);
   return count < 16 ? bits & ((1u << count) - 1u) : bits & 0xFFFFu;
 }
@@ -335,7 +335,7 @@ __device__ __forceinline__ bool tree_seen(const FastArgs& a, const SegRows& s, i
   const int t1 = min(s.nodes, t0 + (kRowsPerBlock + a.H - 1) / a.H);
   const uint32_t* m = a.tree_mask + ((size_t)s.b * a.T + t0) * a.tree_words + (u >> 5);
   uint32_t any = 0;
-  for (int t = t0; t < t1; ++t, m += a.tree_words) any |= __ldg(m);
+  for (int t = t0; t < t1; ++t, m += a.tree_words) any |= *m;
   return (any >> (u & 31)) & 1u;
 }
 
@@ -903,7 +903,7 @@ __device__ __forceinline__ void query_load(const FastArgs& a, const __nv_bfloat1
     for (int e = 0; e < 32; e += 8) {
       uint32_t* d = v[bb] + e;
       if (valid)
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
                      : "l"(row + 64 * (first + bb) + 2 * e));
       else

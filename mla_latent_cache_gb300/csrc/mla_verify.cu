@@ -61,8 +61,8 @@ __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162floa
 // Entries [x, x + 8) of a row (x a multiple of 8); those at or past V are 0.
 __device__ __forceinline__ void load8(const float* row, int x, int V, float (&v)[8]) {
   if (x + 8 <= V) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(row + x));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(row + x + 4));
+    const float4 a = *reinterpret_cast<const float4*>(row + x);
+    const float4 b = *reinterpret_cast<const float4*>(row + x + 4);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   } else {
 #pragma unroll
@@ -71,7 +71,7 @@ __device__ __forceinline__ void load8(const float* row, int x, int V, float (&v)
 }
 __device__ __forceinline__ void load8(const __nv_bfloat16* row, int x, int V, float (&v)[8]) {
   if (x + 8 <= V) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + x));
+    const uint4 u = *reinterpret_cast<const uint4*>(row + x);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

@@ -194,6 +194,158 @@ class SparseStep:
                                     self.workspace, self.ws_bytes, stream), "mla_decode_sparse")
 
 
+def tree_words(parents: np.ndarray):
+    """(mask int32 [B, T, ceil(T/32)], depth int32 [B, T]) of trees given by parents [B, T]
+    (parents[b, t] < t for t > 0; node 0 is the root): node t sees itself and the nodes above
+    it, and sits depth[b, t] positions past the root."""
+    B, T = parents.shape
+    W = (T + 31) // 32
+    see = np.zeros((B, T, 32 * W), dtype=bool)
+    depth = np.zeros((B, T), dtype=np.int32)
+    rows = np.arange(B)
+    for t in range(T):
+        if t:
+            up = parents[:, t]
+            if not ((up >= 0) & (up < t)).all():
+                raise ValueError(f"node {t}: a parent is not an earlier node")
+            see[:, t] = see[rows, up]
+            depth[:, t] = depth[rows, up] + 1
+        see[:, t, t] = True
+    words = (see.reshape(B, T, W, 32).astype(np.uint64) << np.arange(32, dtype=np.uint64)).sum(-1)
+    return words.astype(np.uint32).view(np.int32), depth
+
+
+class SpecStep:
+    """Speculative decoding of one layer over a paged cache that starts empty.
+
+    Each sequence has ``seq_lens`` committed rows.  A step drafts a tree of up to T nodes
+    per sequence (node 0: the last token decided, whose row is not cached yet):
+    ``set_tree`` -> ``attend`` (pages for the nodes' rows, norms + rotation + append,
+    absorption, tree attention, un-absorption), then ``accept`` (verification against the
+    target's probabilities) and ``commit`` (accepted rows moved together, the other pages
+    given back).  Everything runs on the device without a host synchronisation, so a step
+    can be captured in a CUDA graph; ``check`` raises what the device reported.
+    """
+
+    def __init__(self, B: int, H: int, T: int, max_pages: int, num_blocks: int, device="cuda",
+                 cache_format: str = "bf16", interleaved: bool = True, num_slots: int = 0):
+        import torch
+        self.torch = torch
+        dev = self.device = torch.device(device)
+        self.B, self.H, self.T, self.max_pages, self.num_blocks = B, H, T, max_pages, num_blocks
+        self.interleaved = interleaved
+        self.geom = L.make_geom(H)
+        self.batch = L.make_batch(B, T, False, max_pages, num_slots)
+        if cache_format not in ("bf16", "fp8"):
+            raise ValueError(f"cache_format {cache_format!r}")
+        self.cache_format = cache_format
+        if cache_format == "fp8":
+            self.pool = torch.zeros((num_blocks, 64, 656), dtype=torch.uint8, device=dev)
+            self.ws_bytes = L.mla_tree_fp8_workspace_size(self.geom, self.batch)
+        else:
+            self.pool = torch.zeros((num_blocks, 64, 576), dtype=torch.bfloat16, device=dev)
+            self.cache = L.cache_from_pool(self.pool)
+            self.ws_bytes = L.mla_workspace_size(self.geom, self.batch)
+        if self.ws_bytes == 0:
+            raise L.MlaError(L.MLA_ERR_ARG, "mla_workspace_size")
+
+        def i32(*shape, fill=0):
+            return torch.full(shape, fill, dtype=torch.int32, device=dev)
+
+        def bf16(*shape):
+            return torch.empty(shape, dtype=torch.bfloat16, device=dev)
+
+        self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
+        self.refs, self.block_table = i32(num_blocks), i32(B, max_pages, fill=-1)
+        self.seq_lens, self.node_lens, self.tree_lens, self.new_lens = i32(B), i32(B), i32(B), i32(B)
+        self.parents, self.depth, self.mask = i32(B, T), i32(B, T), i32(B, T, (T + 31) // 32)
+        self.accept_len, self.accept_idx, self.out_tokens = i32(B), i32(B, T), i32(B, T)
+        self.nodes = torch.arange(T, dtype=torch.int32, device=dev)
+        self.q_nope, self.q_pe = bf16(B, T, H, 128), bf16(B, T, H, 64)
+        self.q_lat, self.o_lat, self.o = bf16(B, T, H, 512), bf16(B, T, H, 512), bf16(B, T, H, 128)
+        self.lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
+
+    def set_tree(self, parents: np.ndarray, node_lens: np.ndarray):
+        """The step's trees (host arrays): parents [B, T], node_lens [B] (the first node_lens[b] nodes count)."""
+        words, depth = tree_words(np.asarray(parents))
+        for dst, src in ((self.parents, parents), (self.depth, depth), (self.mask, words), (self.node_lens, node_lens)):
+            dst.copy_(self.torch.from_numpy(np.ascontiguousarray(src, dtype=np.int32)))
+
+    def attend(self, q, kv, cos_sin, w_uk, w_uv, q_weight=None, kv_weight=None, eps: float = 1e-6, stream=None):
+        """The nodes' rows into the cache and their attention: q [B, T, H, 192], kv [B, T, 576] -> o [B, T, H, 128].
+
+        (With a stream of its own, make it torch's current one too: the slots are torch's.)"""
+        torch, bt = self.torch, self.block_table
+        N = self.B * self.T
+        torch.add(self.seq_lens, self.node_lens, out=self.new_lens)
+        L.check(L.mla_pages_resize(self.refs, self.num_blocks, bt, self.max_pages, self.max_pages, self.seq_lens,
+                                   self.new_lens, self.B, self.tree_lens, stream), "mla_pages_resize")
+        row = self.seq_lens[:, None] + self.nodes
+        blk = bt.gather(1, (row // 64).clamp(max=self.max_pages - 1).long())
+        slots = torch.where((self.nodes < self.node_lens[:, None]) & (blk >= 0), blk * 64 + row % 64, -1).int()
+        positions = self.seq_lens[:, None] + self.depth
+        args = (self.geom, N, q, q.stride(1), q.stride(2), kv, kv.stride(1), q_weight, kv_weight, eps, cos_sin,
+                cos_sin.shape[0], positions, self.interleaved)
+        tail = (slots, self.q_nope, self.q_pe, stream)
+        if self.cache_format == "fp8":
+            L.check(L.mla_rope_append_fp8(*args, self.pool, self.num_blocks, *tail), "mla_rope_append_fp8")
+        else:
+            L.check(L.mla_rope_append(*args, self.cache, *tail), "mla_rope_append")
+        L.check(L.mla_absorb_q(self.geom, self.q_nope, w_uk, self.q_lat, N, stream), "mla_absorb_q")
+        L.check(L.mla_plan_tree(self.geom, self.batch, self.tree_lens, self.node_lens, self.workspace, self.ws_bytes,
+                                stream), "mla_plan_tree")
+        tail = (bt, self.max_pages, self.tree_lens, self.node_lens, self.mask, 0, self.o_lat, self.lse, self.workspace,
+                self.ws_bytes, stream)
+        if self.cache_format == "fp8":
+            L.check(L.mla_decode_tree_fp8(self.geom, self.batch, self.q_lat, self.q_pe, self.pool, self.num_blocks,
+                                          *tail), "mla_decode_tree_fp8")
+        else:
+            L.check(L.mla_decode_tree(self.geom, self.batch, self.q_lat, self.q_pe, self.cache, *tail),
+                    "mla_decode_tree")
+        L.check(L.mla_unabsorb_o(self.geom, self.o_lat, w_uv, self.o, N, stream), "mla_unabsorb_o")
+        return self.o
+
+    def accept(self, target_probs, draft_probs, tokens, u_accept, u_sample, V: int, stream=None):
+        """Verification: probabilities [B, T, >= V] fp32 or bf16 (draft_probs None: point masses), tokens int32 [B, T]."""
+        dtype = L.MLA_DTYPE_BF16 if target_probs.dtype == self.torch.bfloat16 else L.MLA_DTYPE_F32
+        L.check(L.mla_verify_tree(self.B, self.T, V, target_probs, draft_probs, dtype, target_probs.stride(1), tokens,
+                                  self.parents, self.node_lens, u_accept, u_sample, self.accept_len, self.accept_idx,
+                                  self.out_tokens, stream), "mla_verify_tree")
+        return self.accept_len, self.out_tokens
+
+    def commit(self, stream=None):
+        """The accepted nodes' rows become the sequences' own; the other pages are given back."""
+        args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.node_lens, self.accept_len,
+                self.accept_idx, self.B, self.T, self.new_lens, stream)
+        if self.cache_format == "fp8":
+            L.check(L.mla_cache_compact_fp8(self.pool, self.num_blocks, *args), "mla_cache_compact_fp8")
+        else:
+            L.check(L.mla_cache_compact(self.cache, *args), "mla_cache_compact")
+        L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
+                                   self.tree_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
+
+    def fork(self, src, dst, stream=None):
+        """Sequences dst (int32 device array) become forks of src; what dst held is given back first."""
+        n = src.numel()
+        keep = self.seq_lens.clone()
+        keep[dst.long()] = 0
+        copies = self.torch.empty((3, n), dtype=self.torch.int32, device=self.device)
+        L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
+                                   self.seq_lens, keep, self.B, self.seq_lens, stream), "mla_pages_resize")
+        L.check(L.mla_pages_fork(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
+                                 self.seq_lens, self.B, src, dst, n, copies, stream), "mla_pages_fork")
+        if self.cache_format == "fp8":
+            L.check(L.mla_cache_copy_fp8(self.pool, self.num_blocks, copies, n, stream), "mla_cache_copy_fp8")
+        else:
+            L.check(L.mla_cache_copy(self.cache, copies, n, stream), "mla_cache_copy")
+
+    def check(self, stream=None):
+        """Raise what the device reported since the last check (synchronises)."""
+        status, info = L.mla_read_device_status(self.workspace, stream)
+        if status != L.MLA_OK:
+            raise L.MlaError(status, f"speculative step ({info})")
+
+
 class NormalStep:
     """The Normal (decompressed) arm on one workload: expand the latent cache into
     per-head keys and values (mla_normal_expand), then causal MHA over them

@@ -1,6 +1,7 @@
 """Host-side validation of the speculative step's entry points (no GPU needed): every refusal
 comes before any CUDA call."""
 import numpy as np
+import pytest
 
 from oracle import spec_oracle as O
 
@@ -199,3 +200,14 @@ def test_rotation_oracle_is_a_rotation():
     z = O.rotate_ref(a, cs(3), True)
     c, s = np.cos(3 * inv[4]), np.sin(3 * inv[4])
     assert np.isclose(z[8], a[8] * c - a[9] * s) and np.isclose(z[9], a[9] * c + a[8] * s)
+
+
+def test_tree_words(mla):
+    from mla_latent_cache_gb300.runtime import tree_words
+    par = np.array([[-1, 0, 0, 1, 2, 4], [-1, 0, 1, 2, 3, 4]])
+    words, depth = tree_words(par)
+    see = O.ancestors(par)
+    assert np.array_equal(words[..., 0], (see << np.arange(6)).sum(-1))
+    assert np.array_equal(depth, see.sum(-1) - 1)
+    with pytest.raises(ValueError):
+        tree_words(np.array([[-1, 0, 2]]))
