@@ -72,7 +72,8 @@ typedef struct CUstream_st* mla_stream_t;
 
 typedef enum {
   MLA_OK = 0,
-  MLA_ERR_ARG = -1,          /* null pointer, negative size, unsupported flag */
+  MLA_ERR_ARG = -1,          /* null pointer, negative size, unsupported flag; memory of another device than
+                                the current one (the calls of a speculative step) */
   MLA_ERR_SHAPE = -2,        /* geometry not supported (d_* must be 512/64/128/128, P = 64, 1 <= H <= 128, 128 % H == 0) */
   MLA_ERR_ALIGN = -3,        /* pointer or stride not 16-byte (outputs: 32-byte) aligned */
   MLA_ERR_WORKSPACE = -4,    /* workspace smaller than mla_workspace_size() */

@@ -39,6 +39,15 @@ mla_status check_batch(const mla_batch* b) {
 
 mla_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
+// The calls of a speculative step refuse device memory of another device than the current
+// one, on which they would launch (one array of the call is looked at, ~0.2 us).
+mla_status check_device(const void* p) {
+  cudaPointerAttributes at;
+  int dev = 0;
+  if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+  return at.type == cudaMemoryTypeDevice && at.device != dev ? MLA_ERR_ARG : MLA_OK;
+}
+
 }  // namespace
 
 // Default work-range count: one per CTA pair of the decode kernel (half the SMs).
@@ -256,6 +265,7 @@ mla_status mla_plan_tree(const mla_geom* geom, const mla_batch* batch, const int
   WsLayout L;
   if (!compute_layout(geom, batch, &L)) return MLA_ERR_SHAPE;
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE;
+  if (batch->B > 0 && (s = check_device(seq_lens)) != MLA_OK) return s;
   const TreeNodes tree{node_lens, nullptr};
   return cuda_status(launch_plan(seq_lens, geom, batch, L, workspace, (cudaStream_t)stream, 1, 0, &tree));
 }
@@ -275,6 +285,7 @@ mla_status mla_decode_tree(const mla_geom* geom, const mla_batch* batch, const v
   WsLayout L;
   if (!compute_layout(geom, batch, &L)) return MLA_ERR_SHAPE;
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE;
+  if ((s = check_device(q_lat)) != MLA_OK) return s;
   const TreeNodes tree{node_lens, tree_mask};
   return cuda_status(launch_decode_sm103(geom, batch, L, static_cast<const __nv_bfloat16*>(q_lat),
                                          static_cast<const __nv_bfloat16*>(q_pe), cv, block_table, bt_stride,
@@ -330,6 +341,7 @@ mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, con
   cv.num_blocks = num_blocks;
   const Fp8Pool pool{static_cast<const unsigned char*>(cache_fp8), num_blocks};
   const TreeNodes tree{node_lens, tree_mask};
+  if ((s = check_device(q_lat)) != MLA_OK) return s;
   size_t off_table, off_pool, total;
   if (tree_scratch(geom, batch, L.total, &off_table, &off_pool, &total) && ws_bytes >= total) {
     // each page converted once, then the decode over bf16 pages
@@ -583,6 +595,7 @@ mla_status mla_rope_append(const mla_geom* geom, int N, const void* q, int64_t q
   if (s != MLA_OK || N == 0) return s;
   if ((s = check_cache(cache, &c.cv)) != MLA_OK) return s;
   if ((s = check_rows32(c.cv)) != MLA_OK) return s;
+  if ((s = check_device(q)) != MLA_OK) return s;
   return cuda_status(launch_rope_append(c, (cudaStream_t)stream));
 }
 
@@ -598,6 +611,7 @@ mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64
   if ((s = check_fp8_pool(cache_fp8, num_blocks, &c.cv)) != MLA_OK) return s;
   if ((s = check_rows32(c.cv)) != MLA_OK) return s;
   c.rows_fp8 = static_cast<unsigned char*>(cache_fp8);
+  if ((s = check_device(q)) != MLA_OK) return s;
   return cuda_status(launch_rope_append(c, (cudaStream_t)stream));
 }
 
@@ -616,6 +630,8 @@ mla_status mla_verify_tree(int B, int T, int V, const void* target_probs, const 
       !aligned16(accept_idx) || !aligned16(out_tokens))
     return MLA_ERR_ALIGN;
   if ((row_stride * (dtype == MLA_DTYPE_BF16 ? 2 : 4)) % 16 != 0) return MLA_ERR_ALIGN;
+  const mla_status s = check_device(target_probs);
+  if (s != MLA_OK) return s;
   const VerifyCall c{B, T, V, target_probs, draft_probs, dtype == MLA_DTYPE_BF16, row_stride, tokens, parents,
                      node_lens, u_accept, u_sample, accept_len, accept_idx, out_tokens};
   return cuda_status(launch_verify_tree(c, (cudaStream_t)stream));
@@ -633,8 +649,8 @@ static mla_status cache_compact(const CacheView& cv, void* rows_fp8, const int32
   if (!aligned16(block_table) || !aligned16(seq_lens) || !aligned16(node_lens) || !aligned16(accept_len) ||
       !aligned16(accept_idx) || !aligned16(new_lens))
     return MLA_ERR_ALIGN;
-  const mla_status s = check_rows32(cv);
-  if (s != MLA_OK) return s;
+  mla_status s = check_rows32(cv);
+  if (s != MLA_OK || (s = check_device(block_table)) != MLA_OK) return s;
   return cuda_status(launch_cache_compact(cv, static_cast<unsigned char*>(rows_fp8), block_table, bt_stride, max_pages,
                                           seq_lens, node_lens, accept_len, accept_idx, B, T, new_lens,
                                           (cudaStream_t)stream));
@@ -675,12 +691,13 @@ static mla_status check_pages(const int32_t* refs, int num_blocks, const int32_t
 mla_status mla_pages_resize(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
                             const int32_t* cur_lens, const int32_t* new_lens, int B, int32_t* got_lens,
                             mla_stream_t stream) {
-  const mla_status s = check_pages(refs, num_blocks, block_table, bt_stride, max_pages, B);
+  mla_status s = check_pages(refs, num_blocks, block_table, bt_stride, max_pages, B);
   if (s != MLA_OK) return s;
   if (B > 8192) return MLA_ERR_SHAPE;
   if (B == 0) return MLA_OK;
   if (!cur_lens || !new_lens || !got_lens) return MLA_ERR_ARG;
   if (!aligned16(cur_lens) || !aligned16(new_lens) || !aligned16(got_lens)) return MLA_ERR_ALIGN;
+  if ((s = check_device(refs)) != MLA_OK) return s;
   return cuda_status(launch_pages_resize(refs, num_blocks, block_table, bt_stride, max_pages, cur_lens, new_lens, B,
                                          got_lens, (cudaStream_t)stream));
 }
@@ -688,13 +705,14 @@ mla_status mla_pages_resize(int32_t* refs, int num_blocks, int32_t* block_table,
 mla_status mla_pages_fork(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
                           int32_t* seq_lens, int B, const int32_t* src, const int32_t* dst, int F, int32_t* copies,
                           mla_stream_t stream) {
-  const mla_status s = check_pages(refs, num_blocks, block_table, bt_stride, max_pages, B);
+  mla_status s = check_pages(refs, num_blocks, block_table, bt_stride, max_pages, B);
   if (s != MLA_OK) return s;
   if (F < 0) return MLA_ERR_ARG;
   if (B > 65536 || F > 4096) return MLA_ERR_SHAPE;
   if (F == 0) return MLA_OK;
   if (B == 0 || !seq_lens || !src || !dst || !copies) return MLA_ERR_ARG;
   if (!aligned16(seq_lens) || !aligned16(src) || !aligned16(dst) || !aligned16(copies)) return MLA_ERR_ALIGN;
+  if ((s = check_device(refs)) != MLA_OK) return s;
   return cuda_status(launch_pages_fork(refs, num_blocks, block_table, bt_stride, max_pages, seq_lens, B, src, dst, F,
                                        copies, (cudaStream_t)stream));
 }
@@ -704,8 +722,8 @@ static mla_status cache_copy(const CacheView& cv, void* rows_fp8, const int32_t*
   if (n == 0) return MLA_OK;
   if (!copies) return MLA_ERR_ARG;
   if (!aligned16(copies)) return MLA_ERR_ALIGN;
-  const mla_status s = check_rows32(cv);
-  if (s != MLA_OK) return s;
+  mla_status s = check_rows32(cv);
+  if (s != MLA_OK || (s = check_device(copies)) != MLA_OK) return s;
   return cuda_status(launch_cache_copy(cv, static_cast<unsigned char*>(rows_fp8), copies, n, (cudaStream_t)stream));
 }
 

@@ -19,7 +19,8 @@ namespace mla {
 namespace {
 
 constexpr int kExpandThreads = 256;
-constexpr int kRowsAtOnce = 4;    // rows a warp has in flight
+constexpr int kRowsAtOnce = 4;    // rows a warp has in flight: a CTA's half page in one step
+static_assert(kRowsAtOnce * (kExpandThreads / 32) == kPage / 2, "half a page per step");
 
 struct ExpandArgs {
   const unsigned char* rows;
@@ -40,18 +41,20 @@ __global__ void __launch_bounds__(kExpandThreads) fp8_expand_kernel(ExpandArgs a
   int S = a.seq_lens[b];
   S = S < 0 ? 0 : min(S, a.max_pages * kPage);
   const int pages = (S + kPage - 1) / kPage;
-  for (int p = blockIdx.x; p < pages; p += gridDim.x) {
+  for (int half = blockIdx.x; half < 2 * pages; half += gridDim.x) {
+    const int p = half >> 1, first = (half & 1) * (kPage / 2);
     const int blk = a.block_table[(size_t)b * a.bt_stride + p];
     const bool in_pool = blk >= 0 && blk < a.num_blocks;
     const size_t to = (size_t)b * a.max_pages + p;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && first == 0) {
       a.table[to] = (int)to;
       if (!in_pool && a.checked) record_error(a.hdr, MLA_ERR_DEVICE_CHECK, (b << 16) | p);
     }
-    const int valid = min(kPage, S - p * kPage);
+    const int valid = min(first + kPage / 2, S - p * kPage);
     const unsigned char* src = a.rows + (in_pool ? (size_t)blk * kPage * kFp8RowBytes : 0);
     unsigned char* dst = a.pool + to * kPage * (2 * kDK);
-    for (int r0 = warp; r0 < valid; r0 += kRowsAtOnce * (kExpandThreads / 32)) {
+    {
+      const int r0 = first + warp;
       uint4 code[kRowsAtOnce], rope[kRowsAtOnce];
       float scale[kRowsAtOnce];
 #pragma unroll
@@ -89,7 +92,7 @@ cudaError_t launch_fp8_expand(const Fp8Pool& pool, const int32_t* block_table, i
   // about eight CTAs per SM, shared evenly by the sequences
   const int sms = mla_device_sm_count();
   long long gx = (8LL * (sms > 0 ? sms : 148) + B - 1) / B;
-  if (gx > max_pages) gx = max_pages;
+  if (gx > 2LL * max_pages) gx = 2LL * max_pages;
   return launch_pdl(fp8_expand_kernel, dim3((unsigned)gx, (unsigned)B), dim3(kExpandThreads), 0, st, a);
 }
 

@@ -16,8 +16,10 @@ constexpr int kPlanThreads = 1024;
 // pages 14.4, 1 page 13.6; 4 nodes x 128 heads over 850 rows, plan and decode: 21.9, 20.9,
 // 21.9).
 constexpr int kTreeMinSplitPages = 2;
-// Trees: threads of the planner.  Up to this many groups one per thread, few enough for
-// cheap barriers (one group 4.0 us with 256 threads, 4.9 with 1024; 512 groups 9.9, 8.4).
+// Trees: the least threads of the planner.  A group, and as a rule a segment, per thread,
+// and as few threads as that takes for cheap barriers (one group 4.0 us with 256 threads,
+// 4.9 with 1024; 264 groups 5.9 with 512, 6.3 with 1024; 512 groups 9.9 with 256, 8.6 with
+// 512, 8.4 with 1024).
 constexpr int kTreePlanThreads = 256;
 
 constexpr int kSmemGroups = 4096;   // groups whose segment bases the planner keeps in shared memory
@@ -338,7 +340,9 @@ cudaError_t launch_plan(const int32_t* seq_lens, const mla_geom* g, const mla_ba
   a.tree = tree != nullptr;
   a.node_lens = tree ? tree->node_lens : nullptr;
   a.L = L;
-  const int threads = tree && a.num_groups <= kTreePlanThreads ? kTreePlanThreads : kPlanThreads;
+  int threads = kPlanThreads;
+  if (tree)
+    for (threads = kTreePlanThreads; threads < kPlanThreads && threads < a.num_groups + a.num_groups / 4;) threads *= 2;
   return launch_pdl(plan_kernel, dim3(1), dim3(threads), 0, st, a, reinterpret_cast<char*>(ws));
 }
 
