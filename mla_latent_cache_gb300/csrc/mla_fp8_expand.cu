@@ -14,6 +14,7 @@
 // [16 l, 16 l + 16) (512 contiguous bytes in, 1024 out), lanes 0..7 move the RoPE values.
 #include "mla_fp8.cuh"
 #include "mla_internal.cuh"
+#include "sm103_ptx.cuh"
 
 namespace mla {
 namespace {
@@ -38,12 +39,14 @@ __global__ void __launch_bounds__(kExpandThreads) fp8_expand_kernel(ExpandArgs a
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t* row_blocks = a.block_table + (size_t)b * a.bt_stride;
+  int blk = row_blocks[blockIdx.x >> 1];   // (asked for together with the length; blockIdx.x < 2 max_pages)
   int S = a.seq_lens[b];
   S = S < 0 ? 0 : min(S, a.max_pages * kPage);
   const int pages = (S + kPage - 1) / kPage;
   for (int half = blockIdx.x; half < 2 * pages; half += gridDim.x) {
     const int p = half >> 1, first = (half & 1) * (kPage / 2);
-    const int blk = a.block_table[(size_t)b * a.bt_stride + p];
+    if (half != (int)blockIdx.x) blk = row_blocks[p];
     const bool in_pool = blk >= 0 && blk < a.num_blocks;
     const size_t to = (size_t)b * a.max_pages + p;
     if (threadIdx.x == 0 && first == 0) {
@@ -74,8 +77,8 @@ __global__ void __launch_bounds__(kExpandThreads) fp8_expand_kernel(ExpandArgs a
         const uint2 x = dequant4(code[k].x, s2), y = dequant4(code[k].y, s2);
         const uint2 z = dequant4(code[k].z, s2), w = dequant4(code[k].w, s2);
         unsigned char* out = dst + (size_t)r * (2 * kDK);
-        *reinterpret_cast<uint4*>(out + 32 * lane) = make_uint4(x.x, x.y, y.x, y.y);
-        *reinterpret_cast<uint4*>(out + 32 * lane + 16) = make_uint4(z.x, z.y, w.x, w.y);
+        const uint32_t v[8] = {x.x, x.y, y.x, y.y, z.x, z.y, w.x, w.y};
+        ptx::st_global_v8(out + 32 * lane, v);
         if (lane < 8) *reinterpret_cast<uint4*>(out + 2 * kDLat + 16 * lane) = rope[k];
       }
     }

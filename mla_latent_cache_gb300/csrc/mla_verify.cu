@@ -142,7 +142,7 @@ __device__ __forceinline__ void residual8(const T* p_row, const T* q_row, const 
     load8(q_row, x, V, q);
     if (r.C.hi == 1.f && r.C.lo == 0.f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out[e] = two_sum(clean(p[e]), -clean(q[e]));
+      for (int e = 0; e < 8; ++e) out[e] = quick_sum(clean(p[e]), -clean(q[e]));   // (p < q is cut to 0 below)
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
