@@ -214,3 +214,28 @@ def test_append_on_a_side_stream_and_in_a_graph(mla, cuda):
     g.replay()
     _ok(mla, torch)
     c.check(True)
+
+
+def test_append_at_the_end_of_a_large_pool(mla, cuda):
+    """Rows whose byte offsets pass 32 bits, bf16 and FP8."""
+    import torch
+    c = Case(torch, cuda, 3, 8)
+    small = c.call(mla, True)
+    assert small == mla.MLA_OK
+    rows = c.pool.view(-1, 576)[c.slots.long()].clone()
+    fp8 = torch.zeros((c.nb, 64, 656), dtype=torch.uint8, device=cuda)
+    assert c.call_fp8(mla, True, fp8) == mla.MLA_OK
+    bytes_ = fp8.view(-1, 656)[c.slots.long()].clone()
+    c.nb = 110000                                  # 8.1 GB of bf16 rows, 4.6 GB of FP8 rows
+    c.slots.copy_(torch.tensor([c.nb * 64 - 1, 0, c.nb * 64 - 65], dtype=torch.int32))
+    c.pool = torch.zeros((c.nb, 64, 576), dtype=torch.bfloat16, device=cuda)
+    assert c.call(mla, True) == mla.MLA_OK
+    _ok(mla, torch)
+    flat = c.pool.view(-1, 576)
+    assert torch.equal(torch.stack([flat[int(s)] for s in c.slots]), rows)
+    assert int((flat[1:4096] != 0).sum()) == 0
+    c.pool = flat = None
+    big = torch.zeros((c.nb, 64, 656), dtype=torch.uint8, device=cuda)
+    assert c.call_fp8(mla, True, big) == mla.MLA_OK
+    _ok(mla, torch)
+    assert torch.equal(torch.stack([big.view(-1, 656)[int(s)] for s in c.slots]), bytes_)

@@ -283,3 +283,39 @@ def test_timeouts_are_reported_and_recoverable(mla, cuda, fp8):
     finally:
         mla.check(mla.mla_debug_set_wait_limit(0), "reset wait limit")
     t.run().check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_at_the_end_of_a_large_pool(mla, cuda, fp8):
+    """Blocks whose byte offsets pass 32 bits give the bits of the same pages in a small pool."""
+    import torch
+    t = Tree(mla, torch, cuda, 16, [300, 70], 20, fp8=fp8, sharp=not fp8).run()
+    o, lse = t.o.clone(), t.lse.clone()
+    nb, small = 110000, t.rows if fp8 else t.pool
+    big = torch.zeros((nb, *small.shape[1:]), dtype=small.dtype, device=cuda)
+    big[nb - len(small):] = small
+    t.bt[t.bt >= 0] += nb - len(small)
+    t.rows = big if fp8 else None
+    t.cache = None if fp8 else mla.cache_from_pool(big)
+    t.w.num_blocks = nb
+    t.o.fill_(float("nan"))
+    t.run()
+    assert torch.equal(t.o, o) and torch.equal(t.lse, lse)
+
+
+def test_two_streams_at_once(mla, cuda):
+    """Two trees decoded on two streams with workspaces of their own."""
+    import torch
+    a = Tree(mla, torch, cuda, 128, [2000, 900], 6, seed=1)
+    b = Tree(mla, torch, cuda, 16, [700, 64, 1500], 30, seed=2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for t, s in ((a, s1), (b, s2)):
+            with torch.cuda.stream(s):
+                t.plan()
+                t.decode()
+    torch.cuda.synchronize()
+    for t in (a, b):
+        assert mla.mla_read_device_status(t.ws)[0] == mla.MLA_OK
+        t.check()

@@ -236,3 +236,26 @@ def test_verify_emits_the_targets_distribution(mla, cuda):
     p = p1[0].double().cpu().numpy()
     p /= p.sum()
     assert np.all(np.abs(count - B * p) <= 5 * np.sqrt(B * p * (1 - p)))
+
+
+def test_verify_rows_past_32_bit_offsets(mla, cuda):
+    """Two chains of 1024 nodes over 1.1 million entries (bf16, 4.5 GB): the last row of all decides."""
+    import torch
+    B, T, V = 2, 1024, 1100000
+    p = torch.zeros((B, T, V), dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(0)
+    tokens = rng.integers(0, V, (B, T)).astype(np.int32)
+    tokens[1, -1] = V - 1
+    b, t = np.meshgrid(np.arange(B), np.arange(T - 1), indexing="ij")
+    p[torch.from_numpy(b).cuda(), torch.from_numpy(t).cuda(), torch.from_numpy(tokens[:, 1:]).long().cuda()] = 1
+    p[0, T - 1, 7] = 1
+    p[1, T - 1, V - 3] = 1
+    par = np.tile(np.arange(-1, T - 1, dtype=np.int32), (B, 1))
+    i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    n, idx, out = (torch.full(s, -7, dtype=torch.int32, device="cuda") for s in ((B,), (B, T), (B, T)))
+    assert mla.mla_verify_tree(B, T, V, p, None, mla.MLA_DTYPE_BF16, V, i32(tokens), i32(par), None,
+                               torch.full((B, T), 0.5, device="cuda"), torch.full((B,), 0.5, device="cuda"), n, idx, out) == mla.MLA_OK
+    torch.cuda.synchronize()
+    assert n.tolist() == [T, T]
+    assert torch.equal(idx.cpu(), torch.arange(T, dtype=torch.int32).expand(B, T))
+    assert np.array_equal(out[:, :-1].cpu().numpy(), tokens[:, 1:]) and out[:, -1].tolist() == [7, V - 3]
