@@ -264,8 +264,9 @@ mla_status mla_decode_sparse(const mla_geom* geom, const mla_batch* batch, const
  *   sees, hold finite values; what other rows hold (NaN too) does not matter.
  * mla_plan_tree stands in for mla_plan (the same workspace, size and split rule, but
  * for ranges of at least 2 pages in place of 4; groups past a sequence's nodes need no
- * page), and is re-run when the lengths or node counts change; the mask is the decode's alone.  checked, the
- * status word and every other argument as for mla_decode and mla_decode_fp8.
+ * page; the plan header's MLA_HDR_CAUSAL word is 2), and is re-run when the lengths or node
+ * counts change; the mask is the decode's alone.  checked, the status word and every
+ * other argument as for mla_decode and mla_decode_fp8.
  * mla_decode_tree_fp8 given mla_tree_fp8_workspace_size() bytes (0 on invalid
  * arguments; as much as the batch's longest table as bf16 rows on top of the plan's)
  * converts each page once, ahead of the attention, where a sequence has more than 128
@@ -495,7 +496,7 @@ mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64
  * When no child is left the next token is the first x with R_k(0) + ... + R_k(x) >
  * u_sample * sum R_k (the last x with R_k(x) > 0 if there is none); where R_k is 0
  * everywhere, p takes its place, and where p is too, the token is -1.  Products and
- * sums are fp64.
+ * sums are held as pairs of fp32 values (sums good to about 1e-13 of the mass).
  * Outputs (int32): accept_len[b] = accepted nodes, node 0 included (>= 1; 0 where
  * node_lens[b] = 0); accept_idx[b, 0 .. accept_len) = their indices, increasing;
  * out_tokens[b, 0 .. accept_len) = the tokens decided: those of the accepted nodes
@@ -578,7 +579,8 @@ mla_status mla_cache_copy_fp8(void* cache_fp8, int num_blocks, const int32_t* co
 /* Synchronise `stream`, then return the status word a kernel recorded in the
  * workspace (MLA_OK if none) and, if info != NULL, its detail word.  The
  * workspace-free kernels (absorption, un-absorption, the Normal arm, the gather
- * export, the row append, the verification, the page calls) keep one status word per device, also returned (and cleared) here.
+ * export, the row append, the verification, the page calls) keep one status word per
+ * device, also returned (and cleared) here.
  * With workspace = NULL the call reads that word and then the status and
  * detail words of mla_decode_noalloc's scratch on the current device, returns
  * the first that is set and clears it. */

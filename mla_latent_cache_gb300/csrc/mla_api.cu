@@ -645,7 +645,8 @@ static mla_status cache_compact(const CacheView& cv, void* rows_fp8, const int32
   if (T > kMaxTreeNodes || max_pages >= (1 << 25)) return MLA_ERR_SHAPE;
   if (B == 0) return MLA_OK;
   if (!block_table || !seq_lens || !accept_len || !accept_idx || !new_lens) return MLA_ERR_ARG;
-  if (new_lens == seq_lens || new_lens == node_lens || new_lens == accept_len) return MLA_ERR_ARG;
+  if (new_lens == seq_lens || new_lens == node_lens || new_lens == accept_len || new_lens == accept_idx)
+    return MLA_ERR_ARG;
   if (!aligned16(block_table) || !aligned16(seq_lens) || !aligned16(node_lens) || !aligned16(accept_len) ||
       !aligned16(accept_idx) || !aligned16(new_lens))
     return MLA_ERR_ALIGN;

@@ -223,8 +223,11 @@ class SpecStep:
     ``set_tree`` -> ``attend`` (pages for the nodes' rows, norms + rotation + append,
     absorption, tree attention, un-absorption), then ``accept`` (verification against the
     target's probabilities) and ``commit`` (accepted rows moved together, the other pages
-    given back).  Everything runs on the device without a host synchronisation, so a step
-    can be captured in a CUDA graph; ``check`` raises what the device reported.
+    given back), in this order; ``fork`` between steps.  Everything runs on the device
+    without a host synchronisation, so a step can be captured in a CUDA graph; ``check``
+    raises what the device reported.  A sequence whose nodes get no pages (no free block, or
+    past its table) is reported and sits the step out: outputs 0, accept_len 0, its rows as
+    they were.  Arguments that do not fit raise ValueError before anything is launched.
     """
 
     def __init__(self, B: int, H: int, T: int, max_pages: int, num_blocks: int, device="cuda",
@@ -258,6 +261,8 @@ class SpecStep:
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.refs, self.block_table = i32(num_blocks), i32(B, max_pages, fill=-1)
         self.seq_lens, self.node_lens, self.tree_lens, self.new_lens = i32(B), i32(B), i32(B), i32(B)
+        self.held_lens, self.live = i32(B), i32(B)      # rows that the step's pages hold; nodes that take part
+        self._stage = "attend"
         self.parents, self.depth, self.mask = i32(B, T), i32(B, T), i32(B, T, (T + 31) // 32)
         self.accept_len, self.accept_idx, self.out_tokens = i32(B), i32(B, T), i32(B, T)
         self.nodes = torch.arange(T, dtype=torch.int32, device=dev)
@@ -265,9 +270,39 @@ class SpecStep:
         self.q_lat, self.o_lat, self.o = bf16(B, T, H, 512), bf16(B, T, H, 512), bf16(B, T, H, 128)
         self.lse = torch.empty((B, T, H), dtype=torch.float32, device=dev)
 
+    def _fits(self, name, t, dtypes, shape, rows=False):
+        """t has the shape, one of the types and the device, 16-byte aligned and contiguous; rows: of [B, T]
+        rows that are contiguous, aligned and evenly spaced (the elements from one to the next are returned)."""
+        if t.dtype not in dtypes or t.device.type != self.device.type or t.dim() != len(shape) or any(
+                n is not None and n != m for n, m in zip(shape, t.shape)):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} is not 16-byte aligned")
+        if not rows:
+            if not t.is_contiguous():
+                raise ValueError(f"{name} is not contiguous")
+            return None
+        step = t.stride(1) if self.T > 1 else t.stride(0)
+        if (t.size(-1) > 1 and t.stride(-1) != 1) or (self.B > 1 and self.T > 1 and t.stride(0) != self.T * step) or any(
+                m > 1 and s * t.element_size() % 16 for m, s in zip(t.shape[:-1], t.stride())):
+            raise ValueError(f"{name}: strides {t.stride()}")
+        return step if self.B * self.T > 1 else (t.numel() + 7) // 8 * 8
+
+    def _next(self, stage, after):
+        if self._stage != stage:
+            raise RuntimeError(f"{stage} where {self._stage} is next")
+        self._stage = after
+
     def set_tree(self, parents: np.ndarray, node_lens: np.ndarray):
-        """The step's trees (host arrays): parents [B, T], node_lens [B] (the first node_lens[b] nodes count)."""
-        words, depth = tree_words(np.asarray(parents))
+        """The step's trees (host arrays): parents [B, T], node_lens [B] (the first node_lens[b] nodes count,
+        the other parents are not looked at)."""
+        parents, node_lens = np.asarray(parents), np.asarray(node_lens)
+        if parents.shape != (self.B, self.T) or node_lens.shape != (self.B,):
+            raise ValueError(f"parents {parents.shape}, node_lens {node_lens.shape}")
+        if ((node_lens < 0) | (node_lens > self.T)).any():
+            raise ValueError("a node count outside [0, T]")
+        parents = np.where(np.arange(self.T) < node_lens[:, None], parents, 0)
+        words, depth = tree_words(parents)
         for dst, src in ((self.parents, parents), (self.depth, depth), (self.mask, words), (self.node_lens, node_lens)):
             dst.copy_(self.torch.from_numpy(np.ascontiguousarray(src, dtype=np.int32)))
 
@@ -276,15 +311,28 @@ class SpecStep:
 
         (With a stream of its own, make it torch's current one too: the slots are torch's.)"""
         torch, bt = self.torch, self.block_table
-        N = self.B * self.T
+        B, T, H, N = self.B, self.T, self.H, self.B * self.T
+        bf16, f32 = (torch.bfloat16,), (torch.float32,)
+        q_step = self._fits("q", q, bf16, (B, T, H, 192), rows=True)
+        kv_step = self._fits("kv", kv, bf16, (B, T, 576), rows=True)
+        self._fits("cos_sin", cos_sin, f32, (None, 64))
+        for name, t, shape in (("w_uk", w_uk, (H, 128, 512)), ("w_uv", w_uv, (H, 128, 512)), ("q_weight", q_weight, (192,)),
+                               ("kv_weight", kv_weight, (512,))):
+            if t is not None:
+                self._fits(name, t, bf16, shape)
+        self._next("attend", "accept")
         torch.add(self.seq_lens, self.node_lens, out=self.new_lens)
         L.check(L.mla_pages_resize(self.refs, self.num_blocks, bt, self.max_pages, self.max_pages, self.seq_lens,
-                                   self.new_lens, self.B, self.tree_lens, stream), "mla_pages_resize")
+                                   self.new_lens, self.B, self.held_lens, stream), "mla_pages_resize")
+        granted = self.held_lens == self.new_lens
+        torch.mul(self.node_lens, granted, out=self.live)
+        torch.add(self.seq_lens, self.live, out=self.tree_lens)
         row = self.seq_lens[:, None] + self.nodes
         blk = bt.gather(1, (row // 64).clamp(max=self.max_pages - 1).long())
-        slots = torch.where((self.nodes < self.node_lens[:, None]) & (blk >= 0), blk * 64 + row % 64, -1).int()
-        positions = self.seq_lens[:, None] + self.depth
-        args = (self.geom, N, q, q.stride(1), q.stride(2), kv, kv.stride(1), q_weight, kv_weight, eps, cos_sin,
+        counts = self.nodes < self.live[:, None]
+        slots = torch.where(counts & (blk >= 0), blk * 64 + row % 64, -1).int()
+        positions = torch.where(counts, self.seq_lens[:, None] + self.depth, 0).int()
+        args = (self.geom, N, q, q_step, q.stride(2) if H > 1 else 192, kv, kv_step, q_weight, kv_weight, eps, cos_sin,
                 cos_sin.shape[0], positions, self.interleaved)
         tail = (slots, self.q_nope, self.q_pe, stream)
         if self.cache_format == "fp8":
@@ -292,9 +340,9 @@ class SpecStep:
         else:
             L.check(L.mla_rope_append(*args, self.cache, *tail), "mla_rope_append")
         L.check(L.mla_absorb_q(self.geom, self.q_nope, w_uk, self.q_lat, N, stream), "mla_absorb_q")
-        L.check(L.mla_plan_tree(self.geom, self.batch, self.tree_lens, self.node_lens, self.workspace, self.ws_bytes,
+        L.check(L.mla_plan_tree(self.geom, self.batch, self.tree_lens, self.live, self.workspace, self.ws_bytes,
                                 stream), "mla_plan_tree")
-        tail = (bt, self.max_pages, self.tree_lens, self.node_lens, self.mask, 0, self.o_lat, self.lse, self.workspace,
+        tail = (bt, self.max_pages, self.tree_lens, self.live, self.mask, 0, self.o_lat, self.lse, self.workspace,
                 self.ws_bytes, stream)
         if self.cache_format == "fp8":
             L.check(L.mla_decode_tree_fp8(self.geom, self.batch, self.q_lat, self.q_pe, self.pool, self.num_blocks,
@@ -307,26 +355,42 @@ class SpecStep:
 
     def accept(self, target_probs, draft_probs, tokens, u_accept, u_sample, V: int, stream=None):
         """Verification: probabilities [B, T, >= V] fp32 or bf16 (draft_probs None: point masses), tokens int32 [B, T]."""
-        dtype = L.MLA_DTYPE_BF16 if target_probs.dtype == self.torch.bfloat16 else L.MLA_DTYPE_F32
-        L.check(L.mla_verify_tree(self.B, self.T, V, target_probs, draft_probs, dtype, target_probs.stride(1), tokens,
-                                  self.parents, self.node_lens, u_accept, u_sample, self.accept_len, self.accept_idx,
-                                  self.out_tokens, stream), "mla_verify_tree")
+        torch, B, T = self.torch, self.B, self.T
+        dtype = L.MLA_DTYPE_BF16 if target_probs.dtype == torch.bfloat16 else L.MLA_DTYPE_F32
+        step = self._fits("target_probs", target_probs, (torch.float32, torch.bfloat16), (B, T, None), rows=True)
+        if target_probs.shape[2] < V:
+            raise ValueError(f"target_probs: {target_probs.shape[2]} of {V} entries")
+        if draft_probs is not None and self._fits("draft_probs", draft_probs, (target_probs.dtype,),
+                                                  target_probs.shape, rows=True) != step:
+            raise ValueError(f"draft_probs: strides {draft_probs.stride()}, target_probs: {target_probs.stride()}")
+        self._fits("tokens", tokens, (torch.int32,), (B, T))
+        self._fits("u_accept", u_accept, (torch.float32,), (B, T))
+        self._fits("u_sample", u_sample, (torch.float32,), (B,))
+        self._next("accept", "commit")
+        L.check(L.mla_verify_tree(B, T, V, target_probs, draft_probs, dtype, step, tokens, self.parents, self.live,
+                                  u_accept, u_sample, self.accept_len, self.accept_idx, self.out_tokens, stream),
+                "mla_verify_tree")
         return self.accept_len, self.out_tokens
 
     def commit(self, stream=None):
         """The accepted nodes' rows become the sequences' own; the other pages are given back."""
-        args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.node_lens, self.accept_len,
+        self._next("commit", "attend")
+        args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.live, self.accept_len,
                 self.accept_idx, self.B, self.T, self.new_lens, stream)
         if self.cache_format == "fp8":
             L.check(L.mla_cache_compact_fp8(self.pool, self.num_blocks, *args), "mla_cache_compact_fp8")
         else:
             L.check(L.mla_cache_compact(self.cache, *args), "mla_cache_compact")
         L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
-                                   self.tree_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
+                                   self.held_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
 
     def fork(self, src, dst, stream=None):
-        """Sequences dst (int32 device array) become forks of src; what dst held is given back first."""
+        """Sequences dst (int32 device array, none of them in src) become forks of src; what dst held is given back first."""
         n = src.numel()
+        self._fits("src", src, (self.torch.int32,), (n,))
+        self._fits("dst", dst, (self.torch.int32,), (n,))
+        if self._stage != "attend":
+            raise RuntimeError("fork within a step")
         keep = self.seq_lens.clone()
         keep[dst.long()] = 0
         copies = self.torch.empty((3, n), dtype=self.torch.int32, device=self.device)

@@ -16,12 +16,12 @@ def _np(t):
 
 
 class Harness:
-    def __init__(self, torch, cuda, B, H, T, V, fp8=False, interleaved=True, seed=0):
+    def __init__(self, torch, cuda, B, H, T, V, fp8=False, interleaved=True, seed=0, num_blocks=None):
         from mla_latent_cache_gb300.runtime import SpecStep
         self.torch, self.V = torch, V
         self.rng = np.random.default_rng(seed)
-        self.s = SpecStep(B, H, T, max_pages=8, num_blocks=8 * B, device=cuda, cache_format="fp8" if fp8 else "bf16",
-                          interleaved=interleaved)
+        self.s = SpecStep(B, H, T, max_pages=8, num_blocks=num_blocks or 8 * B, device=cuda,
+                          cache_format="fp8" if fp8 else "bf16", interleaved=interleaved)
         ang = np.arange(600)[:, None] * 10000.0 ** (-np.arange(0, 64, 2) / 64)
         self.table = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
         self.cs = torch.from_numpy(self.table).to(cuda)
@@ -76,6 +76,8 @@ class Harness:
     def values(self, raw):
         """The bf16 values that cached bytes stand for in the attention."""
         torch = self.torch
+        if not len(raw):
+            return np.zeros((0, 576))
         t = torch.from_numpy(raw)
         if self.s.cache_format == "bf16":
             return t.view(torch.bfloat16).double().numpy()
@@ -195,3 +197,82 @@ def test_step_captured_in_a_graph(mla, cuda):
         h.draw_inputs(tree=True)
         g.replay()
         h.check()
+
+
+def test_sequences_without_pages_sit_the_step_out(mla, cuda):
+    """Two of three sequences get the pages of a step: the third answers nothing, keeps its rows
+    and its pages, and goes on when blocks are free again."""
+    import torch
+    h = Harness(torch, cuda, 3, 16, 40, 64, seed=11, num_blocks=5)
+    h.draw_inputs(tree=False)
+    h.n[:] = 40
+    s = h.s
+    s.set_tree(h.par, h.n)
+    h.ua.zero_()
+    h.device_step()
+    h.check()
+    before = [len(r) for r in h.rows]
+    # every sequence holds one block of five; two of them get a second one
+    h.draw_inputs(tree=True)
+    h.n[:] = [40, 40, 40]
+    assert all(0 < n and n + 40 > 64 for n in before)
+    s.set_tree(h.par, h.n)
+    h.device_step()
+    torch.cuda.synchronize()
+    with pytest.raises(mla.MlaError):
+        s.check()
+    assert s.accept_len[2] == 0 and (s.out_tokens[2] == -1).all()
+    assert (s.o[2] == 0).all() and torch.isneginf(s.lse[2]).all()
+    assert s.seq_lens[2] == before[2] and (s.block_table[2] >= 0).sum() == 1
+    assert np.array_equal(h.cached(2, range(before[2])), h.bits[2])
+    lens = s.seq_lens.cpu().numpy()
+    for b in (0, 1):
+        assert lens[b] == before[b] + int(s.accept_len[b]) and s.accept_len[b] > 0
+        assert np.array_equal(h.cached(b, range(before[b])), h.bits[b])
+    # sequence 0 is given back; the other two go on
+    keep = s.seq_lens.clone()
+    keep[0] = 0
+    mla.check(mla.mla_pages_resize(s.refs, s.num_blocks, s.block_table, 8, 8, s.seq_lens, keep, 3, s.seq_lens))
+    for b in range(3):
+        h.bits[b] = h.cached(b, range(int(s.seq_lens[b])))
+        h.rows[b] = h.values(h.bits[b])
+    h.draw_inputs(tree=True)
+    h.n[:] = [3, 9, 40]
+    s.set_tree(h.par, h.n)
+    h.device_step()
+    h.check()
+
+
+def test_one_token_steps_from_strided_views(mla, cuda):
+    """T = 1 (plain decoding): inputs that are views of wider arrays, sequences that take no part."""
+    import torch
+    h = Harness(torch, cuda, 4, 16, 1, 64, seed=13)
+    s = h.s
+    for step in range(3):
+        h.draw_inputs(tree=False)
+        h.n[step] = 0
+        s.set_tree(np.full((4, 1), -1), h.n)
+        wide = torch.full((4, 5, 16, 192), float("nan"), dtype=torch.bfloat16, device=cuda)
+        wide[:, :1] = h.q
+        wide_kv = torch.full((4, 3, 576), float("nan"), dtype=torch.bfloat16, device=cuda)
+        wide_kv[:, :1] = h.kv
+        wide_p = torch.full((4, 2, 80), float("nan"), device=cuda)
+        wide_p[:, :1, :64] = h.p
+        s.attend(wide[:, :1], wide_kv[:, :1], h.cs, *h.w, kv_weight=h.kvw)
+        s.accept(wide_p[:, :1], None, h.tokens, h.ua, h.us, 64)
+        s.commit()
+        assert s.accept_len.cpu().tolist() == h.n.tolist()
+        torch.cuda.synchronize()
+        s.check()
+        qn, qp, rows = O.rope_append_ref(_np(h.q)[:, 0], _np(h.kv)[:, 0], None, _np(h.kvw), 1e-6,
+                                         h.table.astype(np.float64), [len(r) for r in h.rows], s.interleaved)
+        p = h.p.double().cpu().numpy()
+        for b in range(4):
+            raw = h.cached(b, range(int(s.seq_lens[b])))
+            assert np.array_equal(raw[:len(h.bits[b])], h.bits[b]) and len(raw) == len(h.bits[b]) + h.n[b]
+            if h.n[b]:
+                _, nxt = O.verify_ref(p[b], None, np.zeros(1, int), np.array([-1]), 1, np.zeros(1), float(h.us[b]))
+                assert int(s.out_tokens[b, 0]) == nxt
+                mag = np.abs(_np(h.kv)[b]).max() * 2.0 ** -18
+                assert np.all(np.abs(h.values(raw[-1:]) - rows[b]) <= 2.0 ** -8 * np.abs(rows[b]) + mag)
+            h.bits[b], h.rows[b] = raw, h.values(raw)

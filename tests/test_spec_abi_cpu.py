@@ -98,7 +98,7 @@ def test_cache_compact_and_copy_refusals(mla):
             assert call(**{name: None}) == mla.MLA_ERR_ARG, name
         for name in ("bt", "lens", "nodes", "acc", "idx", "new"):
             assert call(**{name: 0x10004}) == mla.MLA_ERR_ALIGN, name
-        for name in ("lens", "nodes", "acc"):     # several CTAs' inputs: the new lengths need their own array
+        for name in ("lens", "nodes", "acc", "idx"):   # several CTAs' inputs: the new lengths need their own array
             assert call(new=ok[name]) == mla.MLA_ERR_ARG, name
         copy = _caller(mla.mla_cache_copy_fp8 if fp8 else mla.mla_cache_copy, first + ["copies", "n"],
                        {**pool, "copies": 0x80000, "n": 3})
