@@ -128,8 +128,25 @@ struct Residual {
   Pair C;                    // > 0: subtract C q
   int num_refused;           // > 0: these tokens are out (point-mass drafts)
   const int* refused;
-  const uint32_t* filter;
+  int cur;                   // the node after which p stands
 };
+// A CTA's shared state.  What is left stands here and not in an argument: a stack frame of
+// a few words per thread is megabytes of local memory a launch (104 bytes: 27 -> 32 us for
+// 64 sequences of 129280 entries).
+struct Shared {
+  Residual left;
+  int want_mass, count;               // told by the walk
+  int cta, t0, t1;                    // told by warp 0 about the draw: the CTA (-1: nothing is left), the tiles that hold the token
+  Pair run, goal;                     // the mass before those tiles, and the one to pass
+  int next;
+  unsigned some_warps;                // bits of the warps that have mass
+  unsigned some[kVerifyWarps];        // of a warp's lanes that have
+  Pair wsum[kVerifyWarps];            // running sums over the CTA's warps
+  Pair lsum[kVerifyThreads];          // running sums over a warp's lanes
+  float2 slice[2][kMaxCluster];       // the CTAs' masses, by turns
+  uint32_t filter[kFilterBits / 32];
+};
+__shared__ Shared sh;
 
 // Entries [x, x + 8) of what is left.
 template <typename T>
@@ -160,7 +177,7 @@ __device__ __forceinline__ void residual8(const T* p_row, const T* q_row, const 
   }
   if (r.num_refused > 0) {
     const int bit = (x >> 3) & (kFilterBits - 1);
-    if ((r.filter[bit >> 5] >> (bit & 31)) & 1u) {
+    if ((sh.filter[bit >> 5] >> (bit & 31)) & 1u) {
       for (int k = 0; k < r.num_refused; ++k) {
         const int e = r.refused[k] - x;
 #pragma unroll
@@ -181,15 +198,21 @@ __device__ __forceinline__ void part_of(int t0, int t1, int k, int n, int* first
 __device__ __forceinline__ Pair shfl(Pair v, int lane) {
   return {__shfl_sync(0xffffffffu, v.hi, lane), __shfl_sync(0xffffffffu, v.lo, lane)};
 }
-// (Called behind a branch that some lanes take, a warp goes through these in two parts that
-// meet at every shuffle: 3300 cycles in place of 550, measured.  So what their callers pass
-// is chosen by selects, find_part adds zeros where a lane has nothing to add, and one
-// lane's stores are followed by __syncwarp.)
 __device__ __forceinline__ Pair keep_if(bool keep, Pair v) { return {keep ? v.hi : 0.f, keep ? v.lo : 0.f}; }
-__device__ __noinline__ Pair warp_sum(Pair v) {
+// The running sums of the first `width` lanes' values (a power of two; later lanes hold no
+// sum), ~110 cycles a step.  Every mass is summed so once, and the search for the drawn
+// token takes what the sums left behind.
+// (Called behind a branch that some lanes take, a warp goes through the steps in two parts
+// that meet at every shuffle: 3300 cycles in place of 550, measured.  So what callers pass
+// is chosen by selects, zeros are added where a lane has nothing to add, and one lane's
+// stores are followed by __syncwarp.)
+__device__ __noinline__ Pair warp_scan(Pair v, int width) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1)
-    v = add(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  for (int o = 1; o < width; o <<= 1) {
+    const Pair y{__shfl_up_sync(0xffffffffu, v.hi, o), __shfl_up_sync(0xffffffffu, v.lo, o)};
+    v = add(v, keep_if(lane >= o, y));
+  }
   return v;
 }
 
@@ -207,12 +230,13 @@ __device__ __forceinline__ Pair residual1(const T* p_row, const T* q_row, const 
   return v;
 }
 
-// The masses (scaled) of the warps' parts of the tiles [t0, t1) into wsum[], of their lanes
-// into lsum[] (the whole CTA).
+// The masses (scaled) of what sh.left leaves of the tiles [t0, t1): the running sums over a
+// warp's lanes into lsum[], which lanes have mass into some[], and (in warp 0, which alone
+// reads them) the running sums over the warps' parts into wsum[].  The whole CTA.
 template <typename T>
-__device__ __noinline__ void part_masses(const T* p_row, const T* q_row, const Residual& r, int V, int t0, int t1,
-                                         Pair* wsum, Pair* lsum) {
+__device__ __noinline__ Pair part_masses(const T* p_row, const T* q_row, int V, int t0, int t1) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const Residual r = sh.left;
   int first, last;
   part_of(t0, t1, w, kVerifyWarps, &first, &last);
   Pair s{0.f, 0.f};
@@ -224,59 +248,45 @@ __device__ __noinline__ void part_masses(const T* p_row, const T* q_row, const R
     for (int e = 0; e < 8; ++e) add_to(s, v[e]);
   }
   s = scaled(quick_sum(s.hi, s.lo), kScale);
-  const Pair all = warp_sum(s);
-  __syncthreads();   // the last readers of wsum and lsum are done
-  lsum[threadIdx.x] = s;
-  if (lane == 0) wsum[w] = all;
+  const unsigned with_mass = __ballot_sync(0xffffffffu, s.hi > 0.f);
+  s = warp_scan(s, 32);
+  __syncthreads();   // the last readers of these arrays are done
+  sh.lsum[threadIdx.x] = s;
+  if (lane == 31) sh.wsum[w] = s;
+  if (lane == 0) sh.some[w] = with_mass;
   __syncthreads();
+  if (w == 0) {
+    s = keep_if(lane < kVerifyWarps, sh.wsum[lane % kVerifyWarps]);
+    const unsigned warps = __ballot_sync(0xffffffffu, s.hi > 0.f);
+    s = warp_scan(s, kVerifyWarps);
+    if (lane < kVerifyWarps) sh.wsum[lane] = s;
+    if (lane == 0) sh.some_warps = warps;
+    __syncwarp();
+    s = shfl(s, kVerifyWarps - 1);
+  }
+  return s;      // warp 0: the CTA's mass
 }
 
-// One warp, lane k holding the mass m of part k (0 past the last): the part that holds
-// the entry at which the running sum, `run` at first, passes `goal`; the last part with
-// mass if rounding leaves none (-1: no mass).  And the sum before that part.
+// One warp, lane k holding the running sum `incl` of the parts up to part k, those in the
+// bits `some` with mass: the part that holds the entry at which the sum, `run` before these
+// parts, passes `goal`; the last part with mass if rounding leaves none (-1: no mass).  And
+// the sum before that part.
 struct Found {
   int part;
   Pair run;
 };
-__device__ __noinline__ Found find_part(Pair m, Pair run, Pair goal) {
-  const int lane = threadIdx.x & 31;
-  Pair incl = m;
-#pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const Pair y{__shfl_up_sync(0xffffffffu, incl.hi, o), __shfl_up_sync(0xffffffffu, incl.lo, o)};
-    incl = add(incl, keep_if(lane >= o, y));
-  }
+__device__ __noinline__ Found find_part(Pair incl, unsigned some, Pair run, Pair goal) {
   incl = add(run, incl);
-  const unsigned some = __ballot_sync(0xffffffffu, m.hi > 0.f);
-  const unsigned hit = __ballot_sync(0xffffffffu, m.hi > 0.f && less(goal, incl));
+  const unsigned hit = __ballot_sync(0xffffffffu, less(goal, incl)) & some;
   const int k = hit ? __ffs(hit) - 1 : 31 - __clz(some);
   const Pair before = shfl(incl, k > 0 ? k - 1 : 0);
   return {k, k > 0 ? before : run};
 }
 
-// What the walking warp tells the others.
-struct Walk {
-  int cur, count, nref, want_mass;
-  Pair C;
-};
-
-// What warp 0 decides about the draw: the CTA (-1: nothing is left), and the tiles that
-// hold the token.
-struct Draw {
-  int cta, t0, t1;
-};
-
 // One cluster of CTAs per sequence.
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a) {
   extern __shared__ int smem[];      // tokens, parents, p(x), q(x), u per node; the path; refused tokens
-  __shared__ Pair wsum[kVerifyWarps];
-  __shared__ float2 slice[2][kMaxCluster];   // the CTAs' masses, by turns
-  __shared__ uint32_t filter[kFilterBits / 32];
-  __shared__ Walk s_walk;
-  __shared__ Pair lsum[kVerifyThreads];
-  __shared__ int s_next;
-  __shared__ Draw s_draw;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   ptx::cluster_sync_all();   // the other CTAs run: their shared memory may be written
   pdl_wait();
@@ -308,26 +318,23 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
     px[t] = fine ? clean(widen(target[(size_t)pr * a.row_stride + x])) : 0.f;
     qx[t] = fine && draft ? clean(widen(draft[(size_t)pr * a.row_stride + x])) : 1.f;
   }
-  for (int k = tid; k < kFilterBits / 32; k += kVerifyThreads) filter[k] = 0;
+  for (int k = tid; k < kFilterBits / 32; k += kVerifyThreads) sh.filter[k] = 0;
   if (bad && rank == 0) atomicCAS(a.status, 0, MLA_ERR_DEVICE_CHECK);
   __syncthreads();
 
-  int t0, t1, turn = 0;
-  part_of(0, (a.V + kTile - 1) / kTile, rank, size, &t0, &t1);
-  const T *p_row = target, *q_row = draft;
-  Residual r;
+  int turn = 0;
 
   // The walk (warp 0), stopping where a refusal asks for the mass left; at its end the draw.
   int cur = 0, at = 0, count = 1, nref = 0;
   const Pair none{0.f, 0.f}, one{kScale, 0.f};
-  Pair C = none, Z = one, run = none, goal = none;   // Z scaled
-  bool stale = false;     // Z has to be summed anew
-  bool bare = false;      // the draw is from p itself
+  Pair C = none, Z = one;   // Z scaled
+  bool stale = false;       // Z has to be summed anew
+  bool bare = false;        // the draw is from p itself
   if (tid == 0) path[0] = 0;
   while (n > 0) {
-    if (warp == 0 && !bare) {
+    if (warp == 0) {
       int want = 0;
-      while (true) {
+      while (!bare) {
         // the next child of cur, in index order
         int child = -1;
         for (int base = at + 1; base < n; base += 32) {
@@ -367,82 +374,94 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
       }
       for (int k = lane; k < nref; k += 32) {     // (at the walk's end only: nobody looks before)
         const int bit = (refused[k] >> 3) & (kFilterBits - 1);
-        if (!want) atomicOr(&filter[bit >> 5], 1u << (bit & 31));
+        if (!want && !bare) atomicOr(&sh.filter[bit >> 5], 1u << (bit & 31));
       }
       __syncwarp();
-      if (lane == 0) s_walk = Walk{cur, count, nref, want, C};
+      if (lane == 0) {
+        sh.left = Residual{bare ? none : C, bare || want ? 0 : nref, refused, cur};
+        sh.want_mass = want;
+        sh.count = count;
+      }
     }
     __syncthreads();
-    const Walk w = s_walk;
-    p_row = target + (size_t)w.cur * a.row_stride;
-    q_row = draft ? draft + (size_t)w.cur * a.row_stride : nullptr;
-    r = Residual{bare ? none : w.C, bare || w.want_mass ? 0 : w.nref, refused, filter};
+    const bool want_mass = sh.want_mass;
     // The mass (scaled) of what is left of the row: lane k of warp 0 gets that of CTA k's slice.
-    part_masses(p_row, q_row, r, a.V, t0, t1, wsum, lsum);
-    if (warp == 0) {
-      const Pair mine = warp_sum(keep_if(lane < kVerifyWarps, wsum[lane % kVerifyWarps]));
-      if (lane < size) {
-        const uint32_t to = ptx::map_to_cta(ptx::smem_addr(&slice[turn][rank]), lane);
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(mine.hi), "f"(mine.lo) : "memory");
-      }
+    int t0, t1;
+    part_of(0, (a.V + kTile - 1) / kTile, rank, size, &t0, &t1);
+    const Pair mine = part_masses(target + (size_t)sh.left.cur * a.row_stride,
+                                  draft ? draft + (size_t)sh.left.cur * a.row_stride : nullptr, a.V, t0, t1);
+    if (warp == 0 && lane < size) {
+      const uint32_t to = ptx::map_to_cta(ptx::smem_addr(&sh.slice[turn][rank]), lane);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(mine.hi), "f"(mine.lo) : "memory");
     }
     __syncwarp();
     ptx::cluster_sync_all();
     if (warp == 0) {
-      const float2 s = slice[turn][lane % kMaxCluster];
+      const float2 s = sh.slice[turn][lane % kMaxCluster];
       const Pair m = keep_if(lane < size, {s.x, s.y});
-      const Pair total = warp_sum(m);
-      Z = total;
+      const unsigned some = __ballot_sync(0xffffffffu, m.hi > 0.f);
+      const Pair slices = warp_scan(m, kMaxCluster);
+      Z = shfl(slices, kMaxCluster - 1);
       stale = false;
       // the draw: the CTA whose slice holds the token, if this was the walk's end
-      int cta = -1;
-      goal = mul(total, {us, 0.f});
-      if (total.hi > 0.f && !w.want_mass) {
-        const Found f = find_part(m, none, goal);
-        cta = f.part;
-        run = f.run;
+      if (!want_mass) {
+        const Pair goal = mul(Z, {us, 0.f});
+        const Found f = find_part(slices, some, none, goal);
+        if (lane == 0) {
+          sh.cta = f.part;
+          sh.t0 = t0;
+          sh.t1 = t1;
+          sh.run = f.run;
+          sh.goal = goal;
+        }
       }
-      if (lane == 0) s_draw = Draw{cta, t0, t1};
     }
     turn ^= 1;
     __syncthreads();
-    if (w.want_mass) continue;
-    if (s_draw.cta >= 0 || bare) break;
+    if (want_mass) continue;
+    if (sh.cta >= 0 || bare) break;
     bare = true;          // nothing is left: p lies under the drafts everywhere
   }
 
   int next = -1, writer = 0;
-  const int count_all = n > 0 ? s_walk.count : 0;
+  const int count_all = n > 0 ? sh.count : 0;
   if (n > 0) {
-    if (s_draw.cta >= 0) writer = s_draw.cta;
-    if (s_draw.cta == rank) {
+    if (sh.cta >= 0) writer = sh.cta;
+    if (sh.cta == rank) {
       // The part of the tiles that holds the token, shared out again until each warp has one
       // tile at most; then its warp's lane, and that lane's entry.
+      const T* p_row = target + (size_t)sh.left.cur * a.row_stride;
+      const T* q_row = draft ? draft + (size_t)sh.left.cur * a.row_stride : nullptr;
       while (true) {
-        const int first = s_draw.t0, last = s_draw.t1;
+        const int first = sh.t0, last = sh.t1;
         __syncthreads();
         if (warp == 0) {
-          const Found w = find_part(keep_if(lane < kVerifyWarps, wsum[lane % kVerifyWarps]), run, goal);
+          const Pair goal = sh.goal;
+          const Found w = find_part(sh.wsum[lane % kVerifyWarps], sh.some_warps, sh.run, goal);
           const int k = max(0, w.part);
-          run = w.run;
           int f, l;
           part_of(first, last, k, kVerifyWarps, &f, &l);
           if (last - first <= kVerifyWarps) {
-            const Found in_tile = find_part(lsum[32 * k + lane], run, goal);
+            const Found in_tile = find_part(sh.lsum[32 * k + lane], sh.some[k], w.run, goal);
             const int x = f * kTile + 8 * max(0, in_tile.part);
             // (a lane past the tile's eight, or the vocabulary, looks at the last entry for nothing)
             const int mine = min(x + min(lane, 7), a.V - 1);
-            const Pair e = keep_if(mine == x + lane, scaled(residual1(p_row, q_row, r, mine), kScale));
-            const Found entry = find_part(e, in_tile.run, goal);
-            if (lane == 0) s_next = x + max(0, entry.part);
+            const Pair e = keep_if(mine == x + lane, scaled(residual1(p_row, q_row, sh.left, mine), kScale));
+            const unsigned some = __ballot_sync(0xffffffffu, e.hi > 0.f);
+            const Found entry = find_part(warp_scan(e, 8), some, in_tile.run, goal);
+            if (lane == 0) sh.next = x + max(0, entry.part);
           }
-          if (lane == 0) s_draw = Draw{rank, f, l};
+          if (lane == 0) {
+            sh.t0 = f;
+            sh.t1 = l;
+            sh.run = w.run;
+          }
         }
         __syncthreads();
         if (last - first <= kVerifyWarps) break;
-        part_masses(p_row, q_row, r, a.V, s_draw.t0, s_draw.t1, wsum, lsum);
+        part_masses(p_row, q_row, a.V, sh.t0, sh.t1);
       }
-      next = s_next;
+      next = sh.next;
     }
   }
   if (rank != writer) return;
