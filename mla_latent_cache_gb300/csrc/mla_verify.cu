@@ -40,6 +40,7 @@ constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kTile = 256;          // vocabulary entries a warp reads at once, 8 per lane
+constexpr int kFirst = 1 << 16;     // next to a parent's number (below kMaxTreeNodes)
 constexpr int kFilterBits = 8192;   // one bit per group of 8 entries (modulo): may hold a refused token
 
 struct VerifyArgs {
@@ -122,6 +123,7 @@ __device__ __forceinline__ bool less(Pair a, Pair b) { return a.hi < b.hi || (a.
 // Masses, and what is compared with them, are held times 2^64: products with a number
 // u >= 2^-24 and their error terms then stay in fp32's range for masses down to its least.
 constexpr float kScale = 18446744073709551616.f, kUnscale = 1.f / kScale;
+constexpr float kHalf = 4294967296.f;   // sqrt(kScale): shared by the factors of a product
 
 // What is left of p: p - C q, or p without the refused tokens.
 struct Residual {
@@ -295,12 +297,18 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
   const int b = blockIdx.x / size;
   const int N = a.T;
   int* tok = smem;
-  int* par = smem + N;
+  int* par = smem + N;               // | kFirst: accepted if it is its parent's first child tried
   float* px = reinterpret_cast<float*>(smem + 2 * N);
   float* qx = reinterpret_cast<float*>(smem + 3 * N);
   float* ua = reinterpret_cast<float*>(smem + 4 * N);
   int* path = smem + 5 * N;
   int* refused = smem + 6 * N;
+  // (a thread's first node is asked for together with the count)
+  int x_first = 0, pr_first = -1;
+  if (tid < N) {
+    x_first = a.tokens[(size_t)b * N + tid];
+    pr_first = a.parents[(size_t)b * N + tid];
+  }
   int n = a.node_lens ? a.node_lens[b] : N;
   const float us = a.u_sample[b];
   bool bad = n < 0 || n > N;
@@ -308,15 +316,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
   const T* target = static_cast<const T*>(a.target) + (size_t)b * N * a.row_stride;
   const T* draft = a.draft ? static_cast<const T*>(a.draft) + (size_t)b * N * a.row_stride : nullptr;
   for (int t = tid; t < n; t += kVerifyThreads) {
-    const int x = a.tokens[(size_t)b * N + t], pr = a.parents[(size_t)b * N + t];
+    const int x = t == tid ? x_first : a.tokens[(size_t)b * N + t];
+    const int pr = t == tid ? pr_first : a.parents[(size_t)b * N + t];
     // A node that can be accepted hangs on an earlier one and holds a token of the vocabulary.
     const bool fine = t > 0 && pr >= 0 && pr < t && x >= 0 && x < a.V;
     bad |= t > 0 && !fine;
     tok[t] = x;
-    par[t] = fine ? pr : -1;
-    ua[t] = a.u_accept[(size_t)b * N + t];
-    px[t] = fine ? clean(widen(target[(size_t)pr * a.row_stride + x])) : 0.f;
-    qx[t] = fine && draft ? clean(widen(draft[(size_t)pr * a.row_stride + x])) : 1.f;
+    const float u = a.u_accept[(size_t)b * N + t];
+    const float p = fine ? clean(widen(target[(size_t)pr * a.row_stride + x])) : 0.f;
+    const float q = fine && draft ? clean(widen(draft[(size_t)pr * a.row_stride + x])) : 1.f;
+    ua[t] = u;
+    px[t] = p;
+    qx[t] = q;
+    const bool first = p > 0.f && less(scaled(two_prod(u * kHalf, q), kHalf), {p * kScale, 0.f});
+    par[t] = fine ? pr | (first ? kFirst : 0) : -1;
   }
   for (int k = tid; k < kFilterBits / 32; k += kVerifyThreads) sh.filter[k] = 0;
   if (bad && rank == 0) atomicCAS(a.status, 0, MLA_ERR_DEVICE_CHECK);
@@ -337,26 +350,38 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
       while (!bare) {
         // the next child of cur, in index order
         int child = -1;
+        bool first = false;
         for (int base = at + 1; base < n; base += 32) {
-          const unsigned m = __ballot_sync(0xffffffffu, base + lane < n && par[base + lane] == cur);
-          if (m) { child = base + __ffs(m) - 1; break; }
+          const int v = base + lane < n ? par[base + lane] : -1;
+          const unsigned m = __ballot_sync(0xffffffffu, (v | kFirst) == (cur | kFirst));
+          const unsigned f = __ballot_sync(0xffffffffu, v >= kFirst);
+          if (m) {
+            child = base + __ffs(m) - 1;
+            first = (f >> (__ffs(m) - 1)) & 1u;
+            break;
+          }
         }
         if (child < 0) break;
         if (stale) { want = 1; break; }
         at = child;
-        const float u = ua[child], p = px[child], q = qx[child];
-        Pair left{p, 0.f};
-        if (draft) {
-          if (C.hi > 0.f) left = sub(left, mul(C, {q, 0.f}));
+        Pair left{px[child], 0.f};
+        bool accepted = first;
+        if (C.hi > 0.f || nref > 0) {        // others were refused here
+          const float u = ua[child], q = qx[child];
+          if (draft) {
+            left = sub(left, mul(C, {q, 0.f}));
+          } else {
+            bool again = false;
+            for (int base = 0; base < nref; base += 32)
+              again |= __any_sync(0xffffffffu, base + lane < nref && refused[base + lane] == tok[child]);
+            if (again) left = none;
+          }
+          left = scaled(left, kScale);
+          accepted = left.hi > 0.f && less(mul(two_prod(u * kHalf, q), scaled(Z, 1.f / kHalf)), left);
         } else {
-          bool again = false;
-          for (int base = 0; base < nref; base += 32)
-            again |= __any_sync(0xffffffffu, base + lane < nref && refused[base + lane] == tok[child]);
-          if (again) left = none;
+          left = scaled(left, kScale);
         }
-        left = scaled(left, kScale);
-        const float half = 4294967296.f;   // sqrt(kScale), shared by the two products
-        if (left.hi > 0.f && less(mul(two_prod(u * half, q), scaled(Z, 1.f / half)), left)) {
+        if (accepted) {
           cur = child;
           if (lane == 0) path[count] = child;
           __syncwarp();
