@@ -30,6 +30,8 @@
 // memory.  Every CTA walks the tree alike (one warp, from shared memory).
 #include <math.h>
 
+#include <atomic>
+
 #include "mla_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -150,15 +152,11 @@ struct Shared {
 };
 __shared__ Shared sh;
 
-// Entries [x, x + 8) of what is left.
-template <typename T>
-__device__ __forceinline__ void residual8(const T* p_row, const T* q_row, const Residual& r, int x, int V,
+// What is left of entries [x, x + 8), from p and (kQ: C > 0) q there.
+template <bool kQ>
+__device__ __forceinline__ void residual8(const float (&p)[8], const float (&q)[8], const Residual& r, int x,
                                           Pair (&out)[8]) {
-  float p[8];
-  load8(p_row, x, V, p);
-  if (r.C.hi > 0.f) {
-    float q[8];
-    load8(q_row, x, V, q);
+  if (kQ) {
     if (r.C.hi == 1.f && r.C.lo == 0.f) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) out[e] = quick_sum(clean(p[e]), -clean(q[e]));   // (p < q is cut to 0 below)
@@ -188,6 +186,27 @@ __device__ __forceinline__ void residual8(const T* p_row, const T* q_row, const 
       }
     }
   }
+}
+
+// This lane's sum of what is left of the tiles [first, last).  One tile at a time: the kernel
+// runs once through most of its code, so that what a longer body gains in loads in flight
+// it loses in instructions to fetch (two tiles at once: 64 chains 23.2 -> 24.4 us, one chain
+// 6.7 -> 8.2 us).
+template <bool kQ, typename T>
+__device__ __forceinline__ Pair sum_tiles(const T* p_row, const T* q_row, const Residual& r, int V, int first, int last) {
+  Pair s{0.f, 0.f};
+#pragma unroll 1
+  for (int t = first; t < last; ++t) {
+    const int x = t * kTile + 8 * (threadIdx.x & 31);
+    float p[8], q[8];
+    Pair v[8];
+    load8(p_row, x, V, p);
+    if (kQ) load8(q_row, x, V, q);
+    residual8<kQ>(p, q, r, x, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) add_to(s, v[e]);
+  }
+  return s;
 }
 
 // Part k of n of the tiles [t0, t1): contiguous, in order.
@@ -241,14 +260,8 @@ __device__ __noinline__ Pair part_masses(const T* p_row, const T* q_row, int V, 
   const Residual r = sh.left;
   int first, last;
   part_of(t0, t1, w, kVerifyWarps, &first, &last);
-  Pair s{0.f, 0.f};
-#pragma unroll 2
-  for (int t = first; t < last; ++t) {
-    Pair v[8];
-    residual8(p_row, q_row, r, t * kTile + 8 * lane, V, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) add_to(s, v[e]);
-  }
+  Pair s = r.C.hi > 0.f ? sum_tiles<true>(p_row, q_row, r, V, first, last)
+                        : sum_tiles<false>(p_row, q_row, r, V, first, last);
   s = scaled(quick_sum(s.hi, s.lo), kScale);
   const unsigned with_mass = __ballot_sync(0xffffffffu, s.hi > 0.f);
   s = warp_scan(s, 32);
@@ -497,28 +510,53 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a)
   if (tid == 0) a.accept_len[b] = count_all;
 }
 
+void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int clusters, int size, size_t smem,
+                    cudaStream_t st) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3((unsigned)(clusters * size));
+  cfg->blockDim = dim3(kVerifyThreads);
+  cfg->dynamicSmemBytes = smem;
+  cfg->stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
+// CTAs per sequence: as many as leave all B clusters resident at once (a cluster lies within
+// a group of SMs, so that is not the slots by the size: 48 clusters of 6 take 16.0 us where
+// 48 of 4 take 12.3, and 44 of 6 take 16.8 where 44 of 4 take 19.4).
+int cluster_size(int B) {
+  // Filled on first use per device; concurrent first calls compute and store the same values.
+  static std::atomic<int> resident[64][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  for (int size = kMaxCluster; size > 1; --size) {
+    int n = resident[dev][size].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg;
+      cudaLaunchAttribute attr[2];
+      cluster_config(&cfg, attr, 64, size, kMaxTreeNodes * 7 * sizeof(int), nullptr);
+      if (cudaOccupancyMaxActiveClusters(&n, verify_kernel<float>, &cfg) != cudaSuccess || n <= 0) n = -1;
+      resident[dev][size].store(n, std::memory_order_relaxed);
+    }
+    if (n >= B) return size;
+  }
+  return 1;
+}
+
 }  // namespace
 
 cudaError_t launch_verify_tree(const VerifyCall& c, cudaStream_t st) {
   VerifyArgs a{c.target, c.draft, c.row_stride, c.tokens, c.parents, c.node_lens, c.u_accept, c.u_sample,
-               c.accept_len, c.accept_idx, c.out_tokens, c.T, c.V, bmm_status_ptr(), 1};
+               c.accept_len, c.accept_idx, c.out_tokens, c.T, c.V, bmm_status_ptr(), cluster_size(c.B)};
   if (!a.status) return cudaErrorInvalidValue;
-  // As many CTAs per sequence as stay resident at once (two per SM).
-  const int slots = 2 * mla_device_sm_count();
-  while (a.cluster < kMaxCluster && (long long)c.B * a.cluster * 2 <= slots) a.cluster *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(c.B * a.cluster));
-  cfg.blockDim = dim3(kVerifyThreads);
-  cfg.dynamicSmemBytes = (size_t)c.T * 7 * sizeof(int);
-  cfg.stream = st;
+  cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cluster_config(&cfg, attr, c.B, a.cluster, (size_t)c.T * 7 * sizeof(int), st);
   return c.bf16 ? cudaLaunchKernelEx(&cfg, verify_kernel<__nv_bfloat16>, a)
                 : cudaLaunchKernelEx(&cfg, verify_kernel<float>, a);
 }
