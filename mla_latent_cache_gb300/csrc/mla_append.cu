@@ -13,7 +13,7 @@
 // it holds the bytes that packing the bf16 row gives).
 //
 // Bound by memory: each value is read once and written once (4096 tokens x 128 heads,
-// 413 MB: 60 us, the copy rate; with the head norm, whose instructions show, 72 us).  A
+// 413 MB: 60 us, the copy rate; with the head norm, whose instructions show, 68 to 70 us).  A
 // warp takes eight heads of a token, or its cache row.
 #include "mla_fp8.cuh"
 #include "mla_internal.cuh"
@@ -21,7 +21,7 @@
 namespace mla {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 constexpr int kDQ = kDNope + kDRope;   // 192
 
 struct AppendArgs {
@@ -177,16 +177,22 @@ __device__ __forceinline__ float sum_squares(const float (&x)[8]) {
 
 // Eight heads per warp: six loads in flight per lane.  Measured at 4096 tokens x 128 heads
 // without norm: 4 heads 69.5 us, 8 heads 60.1 us (6.87 TB/s, the copy rate), 16 heads 60.4;
-// 1 token 1.8, 1.8, 2.3 us.  Three blocks per SM: with the norm and (k, k + 32) pairs that
-// spills a few registers, but two blocks of 109 take 85 us where three take 72.
+// 1 token 1.8, 1.8, 2.3 us.
 constexpr int kQuads = 2;
+// Blocks per SM, six (80 registers) or, with the norm and where all blocks are resident
+// then, five (96): the norm's weights fit in registers, asked for with the rows.  With six
+// they are read again for each four heads, from the L1.  287 tokens x 64 heads: 3.4 us with
+// five, 3.9 with six; 4096 x 128: 74.6 and 70.3 us (with blocks of 256 threads, three of
+// them per SM, 4.3 and 74.2; registers spilled for a launch's first rows cost as much as the
+// rows).
+constexpr int kBlocks = 6, kBlocksKeep = 5;
 
 // Query rows of kQuads x 4 heads of a token by one warp.  Of four heads' 96 chunks a lane
 // holds three: nope chunk lane % 16 of head lane / 16 and of head 2 + lane / 16, and rope
 // chunk lane % 8 of head lane / 8, so that every lane works in every load, and the
 // rotation runs once for four heads.
-template <bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(kAppendThreads, 3) rope_append_kernel(AppendArgs a) {
+template <bool kInterleaved, bool kNorm, bool kKeep>
+__global__ void __launch_bounds__(kAppendThreads, kKeep ? kBlocksKeep : kBlocks) rope_append_kernel(AppendArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -219,7 +225,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) rope_append_kernel(AppendAr
   float cs[8], sn[8];
   load_angles<kInterleaved>(a.cos_sin + (size_t)pos * kDRope, r, cs, sn);
   uint4 wn = zero, wr = zero;
-  if (kNorm) {
+  if (kKeep) {
     wn = *reinterpret_cast<const uint4*>(a.q_weight + 8 * (lane & 15));
     wr = *reinterpret_cast<const uint4*>(a.q_weight + kDNope + 8 * r);
   }
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) rope_append_kernel(AppendAr
       const float inv = rsqrtf((sr + (lane < 16 ? fa : fb)) * (1.f / kDQ) + a.eps);
       const float ia = __shfl_sync(0xffffffffu, inv, (lane & 16) >> 1);
       const float ib = __shfl_sync(0xffffffffu, inv, 16 + ((lane & 16) >> 1));
-      unpack8(wn, w);
+      unpack8(kKeep ? wn : *reinterpret_cast<const uint4*>(a.q_weight + 8 * (lane & 15)), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         xa[e] = xa[e] * ia * w[e];
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) rope_append_kernel(AppendAr
       }
       u[k][0] = pack8(xa);
       u[k][1] = pack8(xb);
-      unpack8(wr, w);
+      unpack8(kKeep ? wr : *reinterpret_cast<const uint4*>(a.q_weight + kDNope + 8 * r), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) xr[e] = xr[e] * inv * w[e];
     }
@@ -274,11 +280,14 @@ cudaError_t launch_rope_append(const AppendCall& c, cudaStream_t st) {
   a.units = (c.H + 4 * kQuads - 1) / (4 * kQuads) + 1;
   const long long ctas = ((long long)c.N * a.units + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   const dim3 grid((unsigned)ctas), block(kAppendThreads);
+  if (c.q_weight && ctas <= (long long)kBlocksKeep * mla_device_sm_count())
+    return c.interleaved ? launch_pdl(rope_append_kernel<true, true, true>, grid, block, 0, st, a)
+                         : launch_pdl(rope_append_kernel<false, true, true>, grid, block, 0, st, a);
   if (c.q_weight)
-    return c.interleaved ? launch_pdl(rope_append_kernel<true, true>, grid, block, 0, st, a)
-                         : launch_pdl(rope_append_kernel<false, true>, grid, block, 0, st, a);
-  return c.interleaved ? launch_pdl(rope_append_kernel<true, false>, grid, block, 0, st, a)
-                       : launch_pdl(rope_append_kernel<false, false>, grid, block, 0, st, a);
+    return c.interleaved ? launch_pdl(rope_append_kernel<true, true, false>, grid, block, 0, st, a)
+                         : launch_pdl(rope_append_kernel<false, true, false>, grid, block, 0, st, a);
+  return c.interleaved ? launch_pdl(rope_append_kernel<true, false, false>, grid, block, 0, st, a)
+                       : launch_pdl(rope_append_kernel<false, false, false>, grid, block, 0, st, a);
 }
 
 }  // namespace mla
