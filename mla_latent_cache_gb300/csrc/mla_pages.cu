@@ -9,6 +9,8 @@
 //
 // Bound: the row moves and page copies by memory (each moved byte is read and written
 // once); the bookkeeping by latency (one CTA: a few thousand integers).
+#include <algorithm>
+
 #include "mla_internal.cuh"
 
 namespace mla {
@@ -17,6 +19,8 @@ namespace {
 constexpr int kBookThreads = 1024;    // the bookkeeping kernels' one CTA
 constexpr int kScanPerThread = 16;    // refs entries per thread and step of the free-block scan
 constexpr int kCopyThreads = 256;
+constexpr int kCompactThreads = 512;
+constexpr int kMaxCompactSplit = 8;   // CTAs per sequence at most
 constexpr int kItems = 8;             // 16-byte pieces a thread holds at once in a row move
 
 // A pool as rows of 16-byte pieces in one or two parts: 64 latent + 8 RoPE pieces of a
@@ -120,11 +124,16 @@ struct CompactArgs {
   int* status;
 };
 
-// One CTA per sequence.  Accepted node idx[i] moves to place i; idx rises strictly, so
-// idx[i] >= i: rows are taken in runs, all of a run's pieces held in registers before any
-// is written, and a later run's sources (idx[j] >= j) lie past an earlier run's places.
-template <int kCols0, int kCols1>
-__global__ void __launch_bounds__(kCopyThreads) compact_kernel(CompactArgs a) {
+// Accepted node idx[i] moves to place i; idx rises strictly, so idx[i] >= i: rows are taken
+// in runs, all of a run's pieces held in registers before any is written, and a later run's
+// sources (idx[j] >= j) lie past an earlier run's places.  Columns of pieces do not meet, so
+// that a sequence's are shared out to as many CTAs (gridDim.y) as there is room for.
+// 512 threads, two CTAs per SM: 256 sequences of up to 48 accepted rows 5.9 us with 256
+// threads, 4.3 with 512; 128 sequences of up to 1000 rows 112 us with one CTA of 256 threads
+// each, 53 with one of 512, 37 with two; 32 sequences of up to 200 rows 9.8 us with one, 3.9
+// with eight.
+template <int kCols0, int kCols1, bool kSplit>
+__global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(CompactArgs a) {
   constexpr int kCols = kCols0 + kCols1;
   extern __shared__ int rows[];          // source and destination row of each accepted node
   pdl_wait();
@@ -136,7 +145,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CompactArgs a) {
   const int S = a.seq_lens[b], n = a.node_lens ? a.node_lens[b] : a.T, acc = a.accept_len[b];
   bool bad = n < 0 || n > a.T || S < n || S > a.max_pages * kPage || acc < 0 || acc > n;
   if (!bad) {
-    for (int i = tid; i < acc; i += kCopyThreads) {
+    for (int i = tid; i < acc; i += kCompactThreads) {
       const int t = i == tid ? t_first : idx[i], prev = i == tid ? prev_first : idx[i - 1];
       if (t <= prev || t >= n) { bad = true; continue; }
       const int from = S - n + t, to = S - n + i;
@@ -150,25 +159,29 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(CompactArgs a) {
   if (__syncthreads_or(bad)) {            // nothing of this sequence is moved
     if (tid == 0) {
       report(a.status);
-      a.new_lens[b] = S;
+      if (blockIdx.y == 0) a.new_lens[b] = S;
     }
     return;
   }
-  if (tid == 0) a.new_lens[b] = S - n + acc;
-  const int items = acc * kCols;
-  for (int base = 0; base < items; base += kCopyThreads * kItems) {
+  if (tid == 0 && blockIdx.y == 0) a.new_lens[b] = S - n + acc;
+  const int col0 = kSplit ? kCols * blockIdx.y / gridDim.y : 0;
+  const int width = kSplit ? kCols * (blockIdx.y + 1) / gridDim.y - col0 : kCols;
+  const int items = acc * width;
+  // i / width for i < 1024 * kCols < 2^17: width < 2^7 is off by less than 2^-15 in 1 / width
+  const unsigned inv = 0xffffffffu / width + 1;
+  for (int base = 0; base < items; base += kCompactThreads * kItems) {
     uint4 v[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      const int it = base + k * kCopyThreads + tid;
-      if (it < items) v[k] = *reinterpret_cast<const uint4*>(piece<kCols0, kCols1>(a.pool, rows[2 * (it / kCols)], it % kCols));
+      const int it = base + k * kCompactThreads + tid, i = kSplit ? (int)__umulhi(it, inv) : it / kCols;
+      if (it < items) v[k] = *reinterpret_cast<const uint4*>(piece<kCols0, kCols1>(a.pool, rows[2 * i], col0 + it - i * width));
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      const int it = base + k * kCopyThreads + tid;
-      if (it < items && rows[2 * (it / kCols)] != rows[2 * (it / kCols) + 1])
-        *reinterpret_cast<uint4*>(piece<kCols0, kCols1>(a.pool, rows[2 * (it / kCols) + 1], it % kCols)) = v[k];
+      const int it = base + k * kCompactThreads + tid, i = kSplit ? (int)__umulhi(it, inv) : it / kCols;
+      if (it < items && rows[2 * i] != rows[2 * i + 1])
+        *reinterpret_cast<uint4*>(piece<kCols0, kCols1>(a.pool, rows[2 * i + 1], col0 + it - i * width)) = v[k];
     }
   }
 }
@@ -467,9 +480,18 @@ cudaError_t launch_cache_compact(const CacheView& cv, unsigned char* rows_fp8, c
   CompactArgs a{row_pool(cv, rows_fp8), block_table, bt_stride, max_pages, seq_lens, node_lens, accept_len, accept_idx,
                 T, new_lens, bmm_status_ptr()};
   if (!a.status) return cudaErrorInvalidValue;
+  // as many CTAs per sequence as stay resident and can have a piece per thread
+  long long split = 2LL * mla_device_sm_count() / B;
+  const long long useful = (long long)T * (rows_fp8 ? 41 : 72) / kCompactThreads;
+  split = std::max(1LL, std::min({split, useful, (long long)kMaxCompactSplit}));
   const size_t smem = (size_t)T * 2 * sizeof(int);
-  return rows_fp8 ? launch_pdl(compact_kernel<41, 0>, dim3(B), dim3(kCopyThreads), smem, st, a)
-                  : launch_pdl(compact_kernel<64, 8>, dim3(B), dim3(kCopyThreads), smem, st, a);
+  const dim3 grid(B, (unsigned)split);
+  const dim3 block(kCompactThreads);
+  if (rows_fp8)
+    return split > 1 ? launch_pdl(compact_kernel<41, 0, true>, grid, block, smem, st, a)
+                     : launch_pdl(compact_kernel<41, 0, false>, grid, block, smem, st, a);
+  return split > 1 ? launch_pdl(compact_kernel<64, 8, true>, grid, block, smem, st, a)
+                   : launch_pdl(compact_kernel<64, 8, false>, grid, block, smem, st, a);
 }
 
 cudaError_t launch_pages_resize(int32_t* refs, int num_blocks, int32_t* block_table, int bt_stride, int max_pages,
