@@ -19,7 +19,8 @@ constexpr int kTreeMinSplitPages = 2;
 // Trees: the least threads of the planner.  A group, and as a rule a segment, per thread,
 // and as few threads as that takes for cheap barriers (one group 4.0 us with 256 threads,
 // 4.9 with 1024; 264 groups 5.9 with 512, 6.3 with 1024; 512 groups 9.9 with 256, 8.6 with
-// 512, 8.4 with 1024).
+// 512, 8.4 with 1024: all with the groups' records read back from the workspace; where they
+// stay in registers 3.8, 4.8 with 512 and 6.3 with 1024).
 constexpr int kTreePlanThreads = 256;
 
 constexpr int kSmemGroups = 4096;   // groups whose segment bases the planner keeps in shared memory
@@ -142,8 +143,8 @@ __device__ __forceinline__ void write_segment(int* seg, int* rptr, int mode, int
     p0 = gs - u; p1 = ge - u;
   }
   int* rec = seg + (size_t)(sb + s) * kSegWords;
-  rec[0] = b; rec[1] = rb; rec[2] = p0; rec[3] = p1; rec[4] = r;
-  rec[5] = (k > 1) ? pb + s : -1; rec[6] = (k > 1) ? mi : -1; rec[7] = 0;
+  *reinterpret_cast<int4*>(rec) = make_int4(b, rb, p0, p1);
+  *reinterpret_cast<int4*>(rec + 4) = make_int4(r, k > 1 ? pb + s : -1, k > 1 ? mi : -1, 0);
   if (mode != 1 || s > 0) {
     rptr[r] = sb + s;     // a cut: the segment starts its range
   } else {
@@ -161,8 +162,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
   int* mrg = reinterpret_cast<int*>(ws + a.L.off_merge);
   int* msync = reinterpret_cast<int*>(ws + a.L.off_merge_sync);
   __shared__ int sh[128];
-  __shared__ int s_sb[kSmemGroups];
   __shared__ int s_q, s_mode, s_U;
+  // Where every group has a thread of its own its record stays in registers, and in shared
+  // memory for the segments' pass.
+  __shared__ int4 s_rec[2][kPlanThreads];
+  int* s_sb = reinterpret_cast<int*>(s_rec);   // otherwise: the groups' first segments
+  static_assert(sizeof(s_rec) >= kSmemGroups * sizeof(int), "room for either");
+  const bool single = a.num_groups <= (int)blockDim.x;
+  int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;   // (pages, pages before, segments, first segment), (first slot, merge record, line position, non-empty before)
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -200,10 +207,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
     block_excl_scan3(v, tot, sh);
     if (g < a.num_groups) {
       const int ne = nonempty_carry + v[1];     // non-empty groups before g
-      grp[g * kGroupWords + 0] = n;
-      grp[g * kGroupWords + 1] = carry + v[0];
-      grp[g * kGroupWords + 6] = carry + v[0] + kSegmentCostPages * ne;   // line position of its first page
-      grp[g * kGroupWords + 7] = ne;
+      rec0.x = n;
+      rec0.y = carry + v[0];
+      rec1.z = carry + v[0] + kSegmentCostPages * ne;   // line position of its first page
+      rec1.w = ne;
+      if (!single) {
+        grp[g * kGroupWords + 0] = rec0.x;
+        grp[g * kGroupWords + 1] = rec0.y;
+        grp[g * kGroupWords + 6] = rec1.z;
+        grp[g * kGroupWords + 7] = rec1.w;
+      }
       nonempty += n > 0;
       maxn = max(maxn, n);
     }
@@ -237,8 +250,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
     const int g = base + tid;
     int k = 0, n = 0;
     if (g < a.num_groups) {
-      n = grp[g * kGroupWords + 0];
-      const int u = grp[g * kGroupWords + 6];
+      if (!single) {
+        rec0 = *reinterpret_cast<const int4*>(grp + g * kGroupWords);
+        rec1 = *reinterpret_cast<const int4*>(grp + g * kGroupWords + 4);
+      }
+      n = rec0.x;
+      const int u = rec1.z;
       if (n > 0) {
         if (mode == 2) k = min(n, a.N);
         else if (mode == 0) k = 1;
@@ -252,11 +269,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
     if (g < a.num_groups) {
       const int sb = cseg + v[0];
       const int pb = part ? cpart + v[1] : -1;
-      grp[g * kGroupWords + 2] = k;
-      grp[g * kGroupWords + 3] = sb;
-      grp[g * kGroupWords + 4] = pb;
-      grp[g * kGroupWords + 5] = mflag ? cmrg + v[2] : -1;
-      if (g < kSmemGroups) s_sb[g] = sb;
+      rec0.z = k;
+      rec0.w = sb;
+      rec1.x = pb;
+      rec1.y = mflag ? cmrg + v[2] : -1;
+      *reinterpret_cast<int4*>(grp + g * kGroupWords) = rec0;
+      *reinterpret_cast<int4*>(grp + g * kGroupWords + 4) = rec1;
+      if (single) {
+        s_rec[0][g] = rec0;
+        s_rec[1][g] = rec1;
+      } else if (g < kSmemGroups) {
+        s_sb[g] = sb;
+      }
       msync[2 * g] = 0;       // merge record g's stored-partial count and merged-row count
       msync[2 * g + 1] = 0;
       if (mflag) {
@@ -278,11 +302,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
       int lo = 0, hi = a.num_groups;        // last group whose first segment is <= i
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_sb[mid] <= i) lo = mid; else hi = mid;
+        if ((single ? s_rec[0][mid].w : s_sb[mid]) <= i) lo = mid; else hi = mid;
       }
       const int g = lo;
-      const int* gr = grp + g * kGroupWords;
-      write_segment(seg, rptr, mode, q, g / a.RB, g % a.RB, gr[0], gr[6], gr[2], gr[3], gr[4], gr[5], i - gr[3], gr[7]);
+      const int4 r0 = single ? s_rec[0][g] : *reinterpret_cast<const int4*>(grp + g * kGroupWords);
+      const int4 r1 = single ? s_rec[1][g] : *reinterpret_cast<const int4*>(grp + g * kGroupWords + 4);
+      write_segment(seg, rptr, mode, q, g / a.RB, g % a.RB, r0.x, r1.z, r0.z, r0.w, r1.x, r1.y, i - r0.w, r1.w);
     }
   } else {
     for (int g = tid; g < a.num_groups; g += blockDim.x) {
@@ -320,7 +345,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
     hdr[MLA_HDR_CAP_PARTIALS] = a.L.cap_partials;
     hdr[MLA_HDR_CAP_RANGES] = a.L.cap_ranges;
     hdr[MLA_HDR_CAP_GROUPS] = a.L.cap_groups;
-    __threadfence();
     hdr[MLA_HDR_MAGIC] = MLA_PLAN_MAGIC;
   }
 }
