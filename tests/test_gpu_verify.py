@@ -1,8 +1,8 @@
 """mla_verify_tree against the float64 rule: accepted nodes and tokens are equal, not near.
 
-Both sides decide in 64 bits, whose sums differ by about 1e-16 of the mass in another
-order of additions; a number lands that close to a border with a probability of about
-1e-11 per decision, so no seed is chosen."""
+The kernel decides in pairs of fp32 values, the oracle in 64 bits; their sums differ by
+about 1e-13 of the mass, and a number lands that close to a border with a probability of
+about 1e-11 per decision, so no seed is chosen."""
 import numpy as np
 import pytest
 
@@ -100,6 +100,14 @@ def test_verify_matches_the_rule(mla, cuda, B, T, V, dtype, draft, tree):
     import torch
     for seed in (0, 1):
         _random(mla, torch, B, T, V, getattr(torch, dtype), draft, tree, seed).check()
+
+
+@pytest.mark.parametrize("B", [20, 37, 44, 50, 60, 75, 90, 140, 310])
+def test_verify_whatever_the_cluster(mla, cuda, B):
+    """Batches that leave room for eight CTAs per sequence, down to one; the last rows of a
+    vocabulary that no slice divides."""
+    import torch
+    _random(mla, torch, B, 4, 5003, torch.float32, B % 2 == 0, False, B).check()
 
 
 @pytest.mark.parametrize("draft", [False, True])
