@@ -9,8 +9,7 @@ A step with drafted tokens has four parts, and each is an operator here:
   verify   acceptance of the drafted tokens against the target's probabilities, from given random
            numbers (mla_verify_tree)
   pages    the cache afterwards: accepted rows moved together (mla_cache_compact); sequences released
-           and forked, full pages shared and the last page copied (mla_pages_resize, mla_pages_fork,
-           mla_cache_copy)
+           and forked, full pages shared and the last page copied (mla_pages_resize, mla_pages_fork)
 
 With ``own`` false, ``run`` computes a case in plain torch operations (32 bits; 64 where a decision
 lies next to a border); with ``own`` true it calls the library.
@@ -250,7 +249,8 @@ def _prepare_fork(case, rng, g):
     keep = lens.copy()
     keep[dst] = 0
     return dict(pool=_normal(g, (nb, PAGE, D_K), 0.1), block_table=_dev(bt), seq_lens=_dev(lens), keep_lens=_dev(keep),
-                refs=_dev(refs), src=_dev(src.astype(np.int32)), dst=_dev(dst.astype(np.int32)))
+                refs=_dev(refs), src=_dev(src.astype(np.int32)), dst=_dev(dst.astype(np.int32)),
+                fork_status=torch.empty((B // 2,), dtype=torch.int32, device=DEV))
 
 
 # --------------------------------------------------------------------------- the library's own handles
@@ -263,8 +263,7 @@ def _handles_tree(s, L):
     c = s["case"]
     s["geom"] = L.make_geom(c["H"])
     s["batch"] = L.make_batch(c["B"], c["T"], False, s["block_table"].shape[1])
-    size = L.mla_tree_fp8_workspace_size if c["fp8"] else L.mla_workspace_size
-    s["ws_bytes"] = size(s["geom"], s["batch"])
+    s["ws_bytes"] = L.mla_workspace_size(s["geom"], s["batch"])
     s["workspace"] = torch.zeros(s["ws_bytes"], dtype=torch.uint8, device=DEV)
     if not c["fp8"]:
         s["cache"] = L.cache_from_pool(s["pool"])
@@ -278,9 +277,7 @@ def _handles_compact(s, L):
     s["cache"] = L.cache_from_pool(s["pool"])
 
 
-def _handles_fork(s, L):
-    s["cache"] = L.cache_from_pool(s["pool"])
-    s["copies"] = torch.empty((3, s["case"]["B"] // 2), dtype=torch.int32, device=DEV)
+_handles_fork = _handles_compact
 
 
 # ------------------------------------------------------------------------------------------------ run
@@ -333,9 +330,8 @@ def _own_fork(s):
     nb = s["pool"].shape[0]
     L.check(L.mla_pages_resize(s["refs"], nb, bt, bt.shape[1], bt.shape[1], s["seq_lens"], s["keep_lens"], B,
                                s["seq_lens"]), "mla_pages_resize")
-    L.check(L.mla_pages_fork(s["refs"], nb, bt, bt.shape[1], bt.shape[1], s["seq_lens"], B, s["src"], s["dst"], B // 2,
-                             s["copies"]), "mla_pages_fork")
-    L.check(L.mla_cache_copy(s["cache"], s["copies"], B // 2), "mla_cache_copy")
+    L.check(L.mla_pages_fork(s["cache"], s["refs"], bt, bt.shape[1], bt.shape[1], s["seq_lens"], B, s["src"], s["dst"],
+                             B // 2, s["fork_status"]), "mla_pages_fork")
     return bt, s["refs"], s["seq_lens"], s["pool"]
 
 
