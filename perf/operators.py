@@ -277,7 +277,9 @@ def _handles_compact(s, L):
     s["cache"] = L.cache_from_pool(s["pool"])
 
 
-_handles_fork = _handles_compact
+def _handles_fork(s, L):
+    s["cache"] = L.cache_from_pool(s["pool"])
+    s["copies"] = torch.empty((3, s["case"]["B"] // 2), dtype=torch.int32, device=DEV)
 
 
 # ------------------------------------------------------------------------------------------------ run
@@ -330,8 +332,9 @@ def _own_fork(s):
     nb = s["pool"].shape[0]
     L.check(L.mla_pages_resize(s["refs"], nb, bt, bt.shape[1], bt.shape[1], s["seq_lens"], s["keep_lens"], B,
                                s["seq_lens"]), "mla_pages_resize")
-    L.check(L.mla_pages_fork(s["cache"], s["refs"], bt, bt.shape[1], bt.shape[1], s["seq_lens"], B, s["src"], s["dst"],
-                             B // 2, s["fork_status"]), "mla_pages_fork")
+    L.check(L.mla_pages_fork(s["refs"], nb, bt, bt.shape[1], bt.shape[1], s["seq_lens"], B, s["src"], s["dst"], B // 2,
+                             s["copies"]), "mla_pages_fork")
+    L.check(L.mla_cache_copy(s["cache"], s["copies"], B // 2), "mla_cache_copy")
     return bt, s["refs"], s["seq_lens"], s["pool"]
 
 
