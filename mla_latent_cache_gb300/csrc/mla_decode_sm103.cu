@@ -896,21 +896,22 @@ __device__ __forceinline__ void reload_role(const Shared& sh, const CUtensorMap*
 // 128 heads is one short segment per node, and with the softmax warps staging the query
 // themselves a segment change took ~14,000 cycles from the last scores to the next ones
 // (of ~1,700 per page): 311 us for 32 trees of up to 16 nodes over 1000 .. 6000 rows, 293
-// with these warps.  The first half of the rows is read ahead, into registers.
+// with these warps.  The first half of the rows is read ahead, into registers, in 16-byte
+// loads: the queries' rows need no more alignment (32-byte loads, which would, take the
+// same time: 32 trees 311.9 us with either, one of 131072 rows 153.8 and 154.1).
 __device__ __forceinline__ void query_load(const FastArgs& a, const __nv_bfloat16* row, bool valid, int first,
                                            uint32_t (&v)[3][32]) {
 #pragma unroll
   for (int bb = 0; bb < 3; ++bb) {
 #pragma unroll
-    for (int e = 0; e < 32; e += 8) {
+    for (int e = 0; e < 32; e += 4) {
       uint32_t* d = v[bb] + e;
       if (valid)
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
                      : "l"(row + 64 * (first + bb) + 2 * e));
       else
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = 0;
+        d[0] = d[1] = d[2] = d[3] = 0;
     }
   }
 }
