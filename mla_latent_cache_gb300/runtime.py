@@ -384,15 +384,27 @@ class SpecStep:
         L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
                                    self.held_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
 
+    def _released(self, src, dst):
+        """Boolean [B]: the sequences that become another's fork, by the rules of mla_pages_fork."""
+        torch, B = self.torch, self.B
+        row = lambda v: torch.where((v >= 0) & (v < B), v, B).long()  # noqa: E731  (B: no sequence)
+        s, d = row(src), row(dst)
+        named = torch.zeros(B + 1, dtype=torch.int32, device=self.device).index_add_(0, d, torch.ones_like(dst))
+        stands = (s < B) & (d < B) & (s != d) & (named[d] == 1) & (named[s] == 0)
+        out = torch.zeros(B + 1, dtype=torch.bool, device=self.device)
+        return out.index_fill_(0, torch.where(stands, d, B), True)[:B]
+
     def fork(self, src, dst, stream=None):
-        """Sequences dst (int32 device array, none of them in src) become forks of src; what dst held is given back first."""
+        """Sequences dst become forks of src (int32 device arrays); what dst held is given back first.  src[f] =
+        dst[f] gives the sequence a last page of its own.  A fork that mla_pages_fork refuses (a number
+        outside [0, B), a dst named twice, a src that is another fork's dst) is reported and changes
+        nothing; one for which no block is left is reported and leaves its dst empty."""
         n = src.numel()
         self._fits("src", src, (self.torch.int32,), (n,))
         self._fits("dst", dst, (self.torch.int32,), (n,))
         if self._stage != "attend":
             raise RuntimeError("fork within a step")
-        keep = self.seq_lens.clone()
-        keep[dst.long()] = 0
+        keep = self.torch.where(self._released(src, dst), 0, self.seq_lens)
         copies = self.torch.empty((3, n), dtype=self.torch.int32, device=self.device)
         L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
                                    self.seq_lens, keep, self.B, self.seq_lens, stream), "mla_pages_resize")

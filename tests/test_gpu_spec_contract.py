@@ -28,3 +28,67 @@ def test_tree_queries_need_16_byte_alignment_only(mla, cuda, fp8):
     t.run()
     assert torch.equal(t.o, o) and torch.equal(t.lse, lse)
     assert np.isfinite(t.o.float().cpu().numpy()).all()
+
+
+def _committed(torch, cuda, lens, B, num_blocks=32, **kw):
+    """A SpecStep whose sequences hold rows of random bytes, and those rows' bytes."""
+    from mla_latent_cache_gb300 import binding as L
+    from mla_latent_cache_gb300.runtime import SpecStep
+    s = SpecStep(B, 16, 4, max_pages=4, num_blocks=num_blocks, device=cuda, **kw)
+    s.pool.view(torch.uint8).random_(0, 100)
+    L.check(L.mla_pages_resize(s.refs, num_blocks, s.block_table, 4, 4, s.seq_lens,
+                               torch.tensor(lens, dtype=torch.int32, device=cuda), B, s.seq_lens))
+    torch.cuda.synchronize()
+    return s
+
+
+def _held(s):
+    """Length, table row and rows' bytes of each sequence."""
+    lens, bt = s.seq_lens.tolist(), s.block_table.cpu().numpy()
+    pool = s.pool.view(s.torch.uint8).cpu().numpy()
+    return {b: (n, bt[b].tolist(), b"".join(pool[bt[b, j // 64], j % 64].tobytes() for j in range(n))) for b, n in enumerate(lens)}
+
+
+def _counts(s):
+    bt = s.block_table.cpu().numpy()
+    assert np.array_equal(np.bincount(bt[bt >= 0], minlength=s.num_blocks), s.refs.cpu().numpy())
+
+
+@pytest.mark.parametrize("src,dst", [([0], [-1]), ([0], [4]), ([0], [2 ** 31 - 1]), ([0], [-2 ** 31]), ([-1], [1]), ([4], [1]),
+                                     ([0, 2], [1, 1]), ([1, 0], [1, 1])])
+def test_refused_forks_change_nothing(mla, cuda, src, dst):
+    import torch
+    s = _committed(torch, cuda, [70, 130, 5, 64], 4)
+    before = _held(s)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda)  # noqa: E731
+    s.fork(i32(src), i32(dst))
+    with pytest.raises(mla.MlaError):
+        s.check()
+    assert _held(s) == before
+    s.fork(i32([*src, 0]), i32([*dst, 3]))          # a good one beside them
+    with pytest.raises(mla.MlaError):
+        s.check()
+    after = _held(s)
+    assert all(after[b] == before[b] for b in (0, 1, 2)) and after[3][0] == 70 and after[3][2] == before[0][2]
+    _counts(s)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_a_sequence_forked_from_itself(mla, cuda, fmt):
+    import torch
+    s = _committed(torch, cuda, [70, 130, 5, 0], 4, cache_format=fmt)
+    before = _held(s)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda)  # noqa: E731
+    s.fork(i32([0, 1, 3]), i32([0, 1, 3]))          # nobody else holds their pages
+    s.check()
+    assert _held(s) == before
+    # sequence 3 takes sequence 1's pages over, last one included, and then a last page of its own
+    s.block_table[3] = s.block_table[1]
+    s.refs[s.block_table[1, :3].long()] += 1
+    s.seq_lens[3] = 130
+    s.fork(i32([3]), i32([3]))
+    s.check()
+    after = _held(s)
+    assert all(after[b] == before[b] for b in (0, 1, 2)) and after[3][2] == before[1][2]
+    assert after[3][1][:2] == before[1][1][:2] and after[3][1][2] != before[1][1][2]
+    _counts(s)
