@@ -7,6 +7,8 @@ un-absorb (o_lat @ W_UV).  Nothing here computes: it allocates and marshals.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 
 from . import binding as L
@@ -228,13 +230,15 @@ class SpecStep:
     raises what the device reported.  A sequence whose nodes get no pages (no free block, or
     past its table) is reported and sits the step out: outputs 0, accept_len 0, its rows as
     they were.  Arguments that do not fit raise ValueError before anything is launched.
+    ``stream`` (a torch stream or its handle; None: torch's current one) is the same for every
+    call of a step, and for the calls between steps.
     """
 
     def __init__(self, B: int, H: int, T: int, max_pages: int, num_blocks: int, device="cuda",
                  cache_format: str = "bf16", interleaved: bool = True, num_slots: int = 0):
         import torch
         self.torch = torch
-        dev = self.device = torch.device(device)
+        dev = torch.device(device)
         self.B, self.H, self.T, self.max_pages, self.num_blocks = B, H, T, max_pages, num_blocks
         self.interleaved = interleaved
         self.geom = L.make_geom(H)
@@ -260,6 +264,7 @@ class SpecStep:
 
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=dev)
         self.refs, self.block_table = i32(num_blocks), i32(B, max_pages, fill=-1)
+        self.device = self.refs.device
         self.seq_lens, self.node_lens, self.tree_lens, self.new_lens = i32(B), i32(B), i32(B), i32(B)
         self.held_lens, self.live = i32(B), i32(B)      # rows that the step's pages hold; nodes that take part
         self._stage = "attend"
@@ -288,12 +293,26 @@ class SpecStep:
             raise ValueError(f"{name}: strides {t.stride()}")
         return step if self.B * self.T > 1 else (t.numel() + 7) // 8 * 8
 
+    def _on(self, stream):
+        """Torch's part of a call goes to the stream that the library's calls take (None: the current one of
+        the step's device), and what it allocates belongs to that stream."""
+        torch = self.torch
+        on = contextlib.ExitStack()
+        if self.device.type == "cuda":
+            if torch.cuda.current_device() != self.device.index:
+                on.enter_context(torch.cuda.device(self.device))
+            if stream is not None:
+                if isinstance(stream, int):
+                    stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+                on.enter_context(torch.cuda.stream(stream))
+        return on
+
     def _next(self, stage, after):
         if self._stage != stage:
             raise RuntimeError(f"{stage} where {self._stage} is next")
         self._stage = after
 
-    def set_tree(self, parents: np.ndarray, node_lens: np.ndarray):
+    def set_tree(self, parents: np.ndarray, node_lens: np.ndarray, stream=None):
         """The step's trees (host arrays): parents [B, T], node_lens [B] (the first node_lens[b] nodes count,
         the other parents are not looked at)."""
         parents, node_lens = np.asarray(parents), np.asarray(node_lens)
@@ -303,13 +322,12 @@ class SpecStep:
             raise ValueError("a node count outside [0, T]")
         parents = np.where(np.arange(self.T) < node_lens[:, None], parents, 0)
         words, depth = tree_words(parents)
-        for dst, src in ((self.parents, parents), (self.depth, depth), (self.mask, words), (self.node_lens, node_lens)):
-            dst.copy_(self.torch.from_numpy(np.ascontiguousarray(src, dtype=np.int32)))
+        with self._on(stream):
+            for dst, src in ((self.parents, parents), (self.depth, depth), (self.mask, words), (self.node_lens, node_lens)):
+                dst.copy_(self.torch.from_numpy(np.ascontiguousarray(src, dtype=np.int32)))
 
     def attend(self, q, kv, cos_sin, w_uk, w_uv, q_weight=None, kv_weight=None, eps: float = 1e-6, stream=None):
-        """The nodes' rows into the cache and their attention: q [B, T, H, 192], kv [B, T, 576] -> o [B, T, H, 128].
-
-        (With a stream of its own, make it torch's current one too: the slots are torch's.)"""
+        """The nodes' rows into the cache and their attention: q [B, T, H, 192], kv [B, T, 576] -> o [B, T, H, 128]."""
         torch, bt = self.torch, self.block_table
         B, T, H, N = self.B, self.T, self.H, self.B * self.T
         bf16, f32 = (torch.bfloat16,), (torch.float32,)
@@ -321,36 +339,37 @@ class SpecStep:
             if t is not None:
                 self._fits(name, t, bf16, shape)
         self._next("attend", "accept")
-        torch.add(self.seq_lens, self.node_lens, out=self.new_lens)
-        L.check(L.mla_pages_resize(self.refs, self.num_blocks, bt, self.max_pages, self.max_pages, self.seq_lens,
-                                   self.new_lens, self.B, self.held_lens, stream), "mla_pages_resize")
-        granted = self.held_lens == self.new_lens
-        torch.mul(self.node_lens, granted, out=self.live)
-        torch.add(self.seq_lens, self.live, out=self.tree_lens)
-        row = self.seq_lens[:, None] + self.nodes
-        blk = bt.gather(1, (row // 64).clamp(max=self.max_pages - 1).long())
-        counts = self.nodes < self.live[:, None]
-        slots = torch.where(counts & (blk >= 0), blk * 64 + row % 64, -1).int()
-        positions = torch.where(counts, self.seq_lens[:, None] + self.depth, 0).int()
-        args = (self.geom, N, q, q_step, q.stride(2) if H > 1 else 192, kv, kv_step, q_weight, kv_weight, eps, cos_sin,
-                cos_sin.shape[0], positions, self.interleaved)
-        tail = (slots, self.q_nope, self.q_pe, stream)
-        if self.cache_format == "fp8":
-            L.check(L.mla_rope_append_fp8(*args, self.pool, self.num_blocks, *tail), "mla_rope_append_fp8")
-        else:
-            L.check(L.mla_rope_append(*args, self.cache, *tail), "mla_rope_append")
-        L.check(L.mla_absorb_q(self.geom, self.q_nope, w_uk, self.q_lat, N, stream), "mla_absorb_q")
-        L.check(L.mla_plan_tree(self.geom, self.batch, self.tree_lens, self.live, self.workspace, self.ws_bytes,
-                                stream), "mla_plan_tree")
-        tail = (bt, self.max_pages, self.tree_lens, self.live, self.mask, 0, self.o_lat, self.lse, self.workspace,
-                self.ws_bytes, stream)
-        if self.cache_format == "fp8":
-            L.check(L.mla_decode_tree_fp8(self.geom, self.batch, self.q_lat, self.q_pe, self.pool, self.num_blocks,
-                                          *tail), "mla_decode_tree_fp8")
-        else:
-            L.check(L.mla_decode_tree(self.geom, self.batch, self.q_lat, self.q_pe, self.cache, *tail),
-                    "mla_decode_tree")
-        L.check(L.mla_unabsorb_o(self.geom, self.o_lat, w_uv, self.o, N, stream), "mla_unabsorb_o")
+        with self._on(stream):
+            torch.add(self.seq_lens, self.node_lens, out=self.new_lens)
+            L.check(L.mla_pages_resize(self.refs, self.num_blocks, bt, self.max_pages, self.max_pages, self.seq_lens,
+                                       self.new_lens, self.B, self.held_lens, stream), "mla_pages_resize")
+            granted = self.held_lens == self.new_lens
+            torch.mul(self.node_lens, granted, out=self.live)
+            torch.add(self.seq_lens, self.live, out=self.tree_lens)
+            row = self.seq_lens[:, None] + self.nodes
+            blk = bt.gather(1, (row // 64).clamp(max=self.max_pages - 1).long())
+            counts = self.nodes < self.live[:, None]
+            slots = torch.where(counts & (blk >= 0), blk * 64 + row % 64, -1).int()
+            positions = torch.where(counts, self.seq_lens[:, None] + self.depth, 0).int()
+            args = (self.geom, N, q, q_step, q.stride(2) if H > 1 else 192, kv, kv_step, q_weight, kv_weight, eps, cos_sin,
+                    cos_sin.shape[0], positions, self.interleaved)
+            tail = (slots, self.q_nope, self.q_pe, stream)
+            if self.cache_format == "fp8":
+                L.check(L.mla_rope_append_fp8(*args, self.pool, self.num_blocks, *tail), "mla_rope_append_fp8")
+            else:
+                L.check(L.mla_rope_append(*args, self.cache, *tail), "mla_rope_append")
+            L.check(L.mla_absorb_q(self.geom, self.q_nope, w_uk, self.q_lat, N, stream), "mla_absorb_q")
+            L.check(L.mla_plan_tree(self.geom, self.batch, self.tree_lens, self.live, self.workspace, self.ws_bytes,
+                                    stream), "mla_plan_tree")
+            tail = (bt, self.max_pages, self.tree_lens, self.live, self.mask, 0, self.o_lat, self.lse, self.workspace,
+                    self.ws_bytes, stream)
+            if self.cache_format == "fp8":
+                L.check(L.mla_decode_tree_fp8(self.geom, self.batch, self.q_lat, self.q_pe, self.pool, self.num_blocks,
+                                              *tail), "mla_decode_tree_fp8")
+            else:
+                L.check(L.mla_decode_tree(self.geom, self.batch, self.q_lat, self.q_pe, self.cache, *tail),
+                        "mla_decode_tree")
+            L.check(L.mla_unabsorb_o(self.geom, self.o_lat, w_uv, self.o, N, stream), "mla_unabsorb_o")
         return self.o
 
     def accept(self, target_probs, draft_probs, tokens, u_accept, u_sample, V: int, stream=None):
@@ -367,22 +386,24 @@ class SpecStep:
         self._fits("u_accept", u_accept, (torch.float32,), (B, T))
         self._fits("u_sample", u_sample, (torch.float32,), (B,))
         self._next("accept", "commit")
-        L.check(L.mla_verify_tree(B, T, V, target_probs, draft_probs, dtype, step, tokens, self.parents, self.live,
-                                  u_accept, u_sample, self.accept_len, self.accept_idx, self.out_tokens, stream),
-                "mla_verify_tree")
+        with self._on(stream):
+            L.check(L.mla_verify_tree(B, T, V, target_probs, draft_probs, dtype, step, tokens, self.parents, self.live,
+                                      u_accept, u_sample, self.accept_len, self.accept_idx, self.out_tokens, stream),
+                    "mla_verify_tree")
         return self.accept_len, self.out_tokens
 
     def commit(self, stream=None):
         """The accepted nodes' rows become the sequences' own; the other pages are given back."""
         self._next("commit", "attend")
-        args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.live, self.accept_len,
-                self.accept_idx, self.B, self.T, self.new_lens, stream)
-        if self.cache_format == "fp8":
-            L.check(L.mla_cache_compact_fp8(self.pool, self.num_blocks, *args), "mla_cache_compact_fp8")
-        else:
-            L.check(L.mla_cache_compact(self.cache, *args), "mla_cache_compact")
-        L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
-                                   self.held_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
+        with self._on(stream):
+            args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.live, self.accept_len,
+                    self.accept_idx, self.B, self.T, self.new_lens, stream)
+            if self.cache_format == "fp8":
+                L.check(L.mla_cache_compact_fp8(self.pool, self.num_blocks, *args), "mla_cache_compact_fp8")
+            else:
+                L.check(L.mla_cache_compact(self.cache, *args), "mla_cache_compact")
+            L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
+                                       self.held_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
 
     def _released(self, src, dst):
         """Boolean [B]: the sequences that become another's fork, by the rules of mla_pages_fork."""
@@ -404,20 +425,22 @@ class SpecStep:
         self._fits("dst", dst, (self.torch.int32,), (n,))
         if self._stage != "attend":
             raise RuntimeError("fork within a step")
-        keep = self.torch.where(self._released(src, dst), 0, self.seq_lens)
-        copies = self.torch.empty((3, n), dtype=self.torch.int32, device=self.device)
-        L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
-                                   self.seq_lens, keep, self.B, self.seq_lens, stream), "mla_pages_resize")
-        L.check(L.mla_pages_fork(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
-                                 self.seq_lens, self.B, src, dst, n, copies, stream), "mla_pages_fork")
-        if self.cache_format == "fp8":
-            L.check(L.mla_cache_copy_fp8(self.pool, self.num_blocks, copies, n, stream), "mla_cache_copy_fp8")
-        else:
-            L.check(L.mla_cache_copy(self.cache, copies, n, stream), "mla_cache_copy")
+        with self._on(stream):
+            keep = self.torch.where(self._released(src, dst), 0, self.seq_lens)
+            copies = self.torch.empty((3, n), dtype=self.torch.int32, device=self.device)
+            L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
+                                       self.seq_lens, keep, self.B, self.seq_lens, stream), "mla_pages_resize")
+            L.check(L.mla_pages_fork(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
+                                     self.seq_lens, self.B, src, dst, n, copies, stream), "mla_pages_fork")
+            if self.cache_format == "fp8":
+                L.check(L.mla_cache_copy_fp8(self.pool, self.num_blocks, copies, n, stream), "mla_cache_copy_fp8")
+            else:
+                L.check(L.mla_cache_copy(self.cache, copies, n, stream), "mla_cache_copy")
 
     def check(self, stream=None):
         """Raise what the device reported since the last check (synchronises)."""
-        status, info = L.mla_read_device_status(self.workspace, stream)
+        with self._on(stream):
+            status, info = L.mla_read_device_status(self.workspace, stream)
         if status != L.MLA_OK:
             raise L.MlaError(status, f"speculative step ({info})")
 

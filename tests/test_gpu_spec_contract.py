@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+from tests.test_gpu_spec_step import Harness
 from tests.test_gpu_tree import Tree
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
@@ -92,3 +93,43 @@ def test_a_sequence_forked_from_itself(mla, cuda, fmt):
     assert all(after[b] == before[b] for b in (0, 1, 2)) and after[3][2] == before[1][2]
     assert after[3][1][:2] == before[1][1][:2] and after[3][1][2] != before[1][1][2]
     _counts(s)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_steps_on_a_stream_of_their_own(mla, cuda, fp8, handle):
+    """Steps and forks given a stream while torch's current one is busy: nothing of them waits for it, and
+    nothing that they keep is taken by what runs there."""
+    import torch
+    h = Harness(torch, cuda, 4, 16, 30, 52, fp8=fp8, seed=4)
+    s, side = h.s, torch.cuda.Stream()
+    st = side.cuda_stream if handle else side
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda)  # noqa: E731
+    src, dst = i32([0, 2, 1]), i32([3, 2, -1])
+    for step in range(6):
+        h.draw_inputs(tree=step % 2 == 1)
+        par, n = h.par, h.n
+        s.set_tree(np.tile(np.arange(-1, 29), (4, 1)), np.full(4, 1))   # not this step's
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)                # ~50 ms
+        busy = [torch.full((4, 30), -1, dtype=torch.int32, device=cuda) for _ in range(40)]
+        s.set_tree(par, n, stream=st)
+        s.attend(h.q, h.kv, h.cs, *h.w, kv_weight=h.kvw, stream=st)
+        s.accept(h.p, h.d, h.tokens, h.ua, h.us, h.V, stream=st)
+        s.commit(stream=st)
+        side.synchronize()
+        assert step < 2 or not torch.cuda.current_stream().query()    # (first uses load kernels, which may wait)
+        h.check()
+        del busy
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        s.fork(src, dst, stream=st)
+        busy = [torch.full((4,), 1 << 20, dtype=torch.int32, device=cuda) for _ in range(40)]
+        side.synchronize()
+        assert step < 2 or not torch.cuda.current_stream().query()
+        with pytest.raises(mla.MlaError):             # (the fork to -1)
+            s.check(stream=st)
+        h.rows[3], h.bits[3] = h.rows[0].copy(), h.bits[0].copy()
+        del busy
+    _counts(s)
+    assert max(len(r) for r in h.rows) > 6
