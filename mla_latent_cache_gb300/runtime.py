@@ -8,6 +8,7 @@ un-absorb (o_lat @ W_UV).  Nothing here computes: it allocates and marshals.
 from __future__ import annotations
 
 import contextlib
+import math
 
 import numpy as np
 
@@ -245,6 +246,9 @@ class SpecStep:
         self.batch = L.make_batch(B, T, False, max_pages, num_slots)
         if cache_format not in ("bf16", "fp8"):
             raise ValueError(f"cache_format {cache_format!r}")
+        if not (0 <= B <= 8192 and 1 <= T <= 1024 and 1 <= num_blocks < 1 << 25 and 1 <= max_pages < 1 << 25
+                and B * max_pages < 1 << 31 and B * T * (H + 1) < 1 << 31):
+            raise ValueError(f"B {B}, T {T}, H {H}, max_pages {max_pages}, num_blocks {num_blocks}")
         self.cache_format = cache_format
         if cache_format == "fp8":
             self.pool = torch.zeros((num_blocks, 64, 656), dtype=torch.uint8, device=dev)
@@ -267,7 +271,7 @@ class SpecStep:
         self.device = self.refs.device
         self.seq_lens, self.node_lens, self.tree_lens, self.new_lens = i32(B), i32(B), i32(B), i32(B)
         self.held_lens, self.live = i32(B), i32(B)      # rows that the step's pages hold; nodes that take part
-        self._stage = "attend"
+        self._stage, self._moved = "attend", False
         self.parents, self.depth, self.mask = i32(B, T), i32(B, T), i32(B, T, (T + 31) // 32)
         self.accept_len, self.accept_idx, self.out_tokens = i32(B), i32(B, T), i32(B, T)
         self.nodes = torch.arange(T, dtype=torch.int32, device=dev)
@@ -278,7 +282,7 @@ class SpecStep:
     def _fits(self, name, t, dtypes, shape, rows=False):
         """t has the shape, one of the types and the device, 16-byte aligned and contiguous; rows: of [B, T]
         rows that are contiguous, aligned and evenly spaced (the elements from one to the next are returned)."""
-        if t.dtype not in dtypes or t.device.type != self.device.type or t.dim() != len(shape) or any(
+        if t.dtype not in dtypes or t.device != self.device or t.dim() != len(shape) or any(
                 n is not None and n != m for n, m in zip(shape, t.shape)):
             raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}")
         if t.data_ptr() % 16:
@@ -291,7 +295,7 @@ class SpecStep:
         if (t.size(-1) > 1 and t.stride(-1) != 1) or (self.B > 1 and self.T > 1 and t.stride(0) != self.T * step) or any(
                 m > 1 and s * t.element_size() % 16 for m, s in zip(t.shape[:-1], t.stride())):
             raise ValueError(f"{name}: strides {t.stride()}")
-        return step if self.B * self.T > 1 else (t.numel() + 7) // 8 * 8
+        return step if self.B * self.T > 1 else (math.prod(t.shape[2:]) + 7) // 8 * 8
 
     def _on(self, stream):
         """Torch's part of a call goes to the stream that the library's calls take (None: the current one of
@@ -307,9 +311,13 @@ class SpecStep:
                 on.enter_context(torch.cuda.stream(stream))
         return on
 
-    def _next(self, stage, after):
+    @contextlib.contextmanager
+    def _part(self, stage, after, stream):
+        """One part of the step, on `stream`; what fails leaves the step where it was."""
         if self._stage != stage:
             raise RuntimeError(f"{stage} where {self._stage} is next")
+        with self._on(stream):
+            yield
         self._stage = after
 
     def set_tree(self, parents: np.ndarray, node_lens: np.ndarray, stream=None):
@@ -334,15 +342,18 @@ class SpecStep:
         q_step = self._fits("q", q, bf16, (B, T, H, 192), rows=True)
         kv_step = self._fits("kv", kv, bf16, (B, T, 576), rows=True)
         self._fits("cos_sin", cos_sin, f32, (None, 64))
+        if not eps >= 0 or cos_sin.shape[0] < 1:
+            raise ValueError(f"eps {eps}, {cos_sin.shape[0]} positions")
         for name, t, shape in (("w_uk", w_uk, (H, 128, 512)), ("w_uv", w_uv, (H, 128, 512)), ("q_weight", q_weight, (192,)),
                                ("kv_weight", kv_weight, (512,))):
             if t is not None:
                 self._fits(name, t, bf16, shape)
-        self._next("attend", "accept")
-        with self._on(stream):
+        with self._part("attend", "accept", stream), contextlib.ExitStack() as undo:
             torch.add(self.seq_lens, self.node_lens, out=self.new_lens)
             L.check(L.mla_pages_resize(self.refs, self.num_blocks, bt, self.max_pages, self.max_pages, self.seq_lens,
                                        self.new_lens, self.B, self.held_lens, stream), "mla_pages_resize")
+            undo.callback(L.mla_pages_resize, self.refs, self.num_blocks, bt, self.max_pages, self.max_pages,
+                          self.held_lens, self.seq_lens, self.B, self.new_lens, stream)
             granted = self.held_lens == self.new_lens
             torch.mul(self.node_lens, granted, out=self.live)
             torch.add(self.seq_lens, self.live, out=self.tree_lens)
@@ -370,6 +381,7 @@ class SpecStep:
                 L.check(L.mla_decode_tree(self.geom, self.batch, self.q_lat, self.q_pe, self.cache, *tail),
                         "mla_decode_tree")
             L.check(L.mla_unabsorb_o(self.geom, self.o_lat, w_uv, self.o, N, stream), "mla_unabsorb_o")
+            undo.pop_all()
         return self.o
 
     def accept(self, target_probs, draft_probs, tokens, u_accept, u_sample, V: int, stream=None):
@@ -377,16 +389,15 @@ class SpecStep:
         torch, B, T = self.torch, self.B, self.T
         dtype = L.MLA_DTYPE_BF16 if target_probs.dtype == torch.bfloat16 else L.MLA_DTYPE_F32
         step = self._fits("target_probs", target_probs, (torch.float32, torch.bfloat16), (B, T, None), rows=True)
-        if target_probs.shape[2] < V:
-            raise ValueError(f"target_probs: {target_probs.shape[2]} of {V} entries")
+        if not 1 <= V <= min(target_probs.shape[2], 1 << 30) or step < V:
+            raise ValueError(f"target_probs: {target_probs.shape[2]} entries {step} apart, of {V}")
         if draft_probs is not None and self._fits("draft_probs", draft_probs, (target_probs.dtype,),
                                                   target_probs.shape, rows=True) != step:
             raise ValueError(f"draft_probs: strides {draft_probs.stride()}, target_probs: {target_probs.stride()}")
         self._fits("tokens", tokens, (torch.int32,), (B, T))
         self._fits("u_accept", u_accept, (torch.float32,), (B, T))
         self._fits("u_sample", u_sample, (torch.float32,), (B,))
-        self._next("accept", "commit")
-        with self._on(stream):
+        with self._part("accept", "commit", stream):
             L.check(L.mla_verify_tree(B, T, V, target_probs, draft_probs, dtype, step, tokens, self.parents, self.live,
                                       u_accept, u_sample, self.accept_len, self.accept_idx, self.out_tokens, stream),
                     "mla_verify_tree")
@@ -394,16 +405,18 @@ class SpecStep:
 
     def commit(self, stream=None):
         """The accepted nodes' rows become the sequences' own; the other pages are given back."""
-        self._next("commit", "attend")
-        with self._on(stream):
-            args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.live, self.accept_len,
-                    self.accept_idx, self.B, self.T, self.new_lens, stream)
-            if self.cache_format == "fp8":
-                L.check(L.mla_cache_compact_fp8(self.pool, self.num_blocks, *args), "mla_cache_compact_fp8")
-            else:
-                L.check(L.mla_cache_compact(self.cache, *args), "mla_cache_compact")
+        with self._part("commit", "attend", stream):
+            if not self._moved:       # (moving the rows twice would mix them)
+                args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.live, self.accept_len,
+                        self.accept_idx, self.B, self.T, self.new_lens, stream)
+                if self.cache_format == "fp8":
+                    L.check(L.mla_cache_compact_fp8(self.pool, self.num_blocks, *args), "mla_cache_compact_fp8")
+                else:
+                    L.check(L.mla_cache_compact(self.cache, *args), "mla_cache_compact")
+                self._moved = True
             L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
                                        self.held_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
+            self._moved = False
 
     def _released(self, src, dst):
         """Boolean [B]: the sequences that become another's fork, by the rules of mla_pages_fork."""

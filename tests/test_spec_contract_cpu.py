@@ -121,3 +121,86 @@ def test_a_sequence_forked_from_itself_keeps_its_rows(step, lib):
     assert after[0] == before[0] and after[1][0] == 70
     assert after[1][1][0] == before[0][1][0] and after[1][1][1] not in before[0][1]
     O.Pages(s.block_table.numpy(), s.refs.numpy(), s.seq_lens.numpy()).check()
+
+
+def _inputs(s, V=60):
+    z = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    B, T, H = s.B, s.T, s.H
+    return (dict(q=z(B, T, H, 192), kv=z(B, T, 576), cos_sin=z(64, 64, dtype=torch.float32), w_uk=z(H, 128, 512),
+                 w_uv=z(H, 128, 512), kv_weight=z(512)),
+            dict(target_probs=torch.zeros(B, T, 64), draft_probs=None, tokens=torch.zeros(B, T, dtype=torch.int32),
+                 u_accept=torch.zeros(B, T), u_sample=torch.zeros(B), V=V))
+
+
+def test_what_a_call_would_refuse_is_refused_before_anything_runs(step, lib):
+    s = step(lens=[70, 5])
+    attend, accept = _inputs(s)
+    before = _pages(s)
+    for bad in (dict(eps=-1.0), dict(eps=float("nan")), dict(cos_sin=torch.zeros(0, 64)),
+                dict(q=torch.zeros(2, 4, 16, 192, dtype=torch.bfloat16, device="meta"))):
+        with pytest.raises(ValueError):
+            s.attend(**{**attend, **bad})
+    assert lib.calls == [] and _pages(s) == before
+    s.attend(**attend)
+    lib.calls.clear()
+    for bad in (dict(V=0), dict(V=-3), dict(V=65), dict(target_probs=torch.zeros(1, 1, 64).expand(2, 4, 64)),
+                dict(draft_probs=torch.zeros(2, 4, 64, device="meta"))):
+        with pytest.raises(ValueError):
+            s.accept(**{**accept, **bad})
+    assert lib.calls == []
+    s.accept(**accept)                        # the step goes on as if nothing had been asked
+    s.commit()
+
+
+def test_sizes_that_no_call_takes(lib):
+    from mla_latent_cache_gb300.runtime import SpecStep
+    ok = dict(B=2, H=16, T=4, max_pages=4, num_blocks=8, device="cpu")
+    SpecStep(**ok)
+    for bad in (dict(T=0), dict(T=1025), dict(B=8193), dict(B=-1), dict(num_blocks=0), dict(num_blocks=1 << 25),
+                dict(max_pages=0), dict(max_pages=1 << 25)):
+        with pytest.raises(ValueError):
+            SpecStep(**{**ok, **bad})
+
+
+@pytest.mark.parametrize("name,answer", [("mla_rope_append", -1), ("mla_absorb_q", -6), ("mla_plan_tree", -2),
+                                         ("mla_decode_tree", -6), ("mla_unabsorb_o", MemoryError()),
+                                         ("mla_rope_append", KeyboardInterrupt())])
+def test_a_failed_attend_gives_its_pages_back(step, lib, mla, name, answer):
+    s = step(lens=[62, 130], T=8)
+    s.set_tree(np.tile(np.arange(-1, 7), (2, 1)), np.array([8, 3]))
+    attend, accept = _inputs(s)
+    before, refs = _pages(s), s.refs.tolist()
+    lib.answers[name] = answer
+    with pytest.raises(mla.MlaError if isinstance(answer, int) else type(answer)):
+        s.attend(**attend)
+    assert _pages(s) == before and s.refs.tolist() == refs
+    with pytest.raises(RuntimeError):
+        s.accept(**accept)                    # nothing is attended
+    lib.answers.clear()
+    s.attend(**attend)
+    assert s.held_lens.tolist() == [70, 133] and int((s.block_table[0] >= 0).sum()) == 2
+    O.Pages(s.block_table.numpy(), s.refs.numpy(), s.held_lens.numpy()).check()
+
+
+def test_failed_accept_and_commit_can_be_repeated(step, lib, mla):
+    s = step(lens=[62, 130])
+    attend, accept = _inputs(s)
+    s.attend(**attend)
+    lib.answers["mla_verify_tree"] = -6
+    with pytest.raises(mla.MlaError):
+        s.accept(**accept)
+    with pytest.raises(RuntimeError):
+        s.commit()
+    lib.answers["mla_verify_tree"] = 0
+    s.accept(**accept)
+    lib.answers["mla_cache_compact"] = -6
+    with pytest.raises(mla.MlaError):
+        s.commit()
+    lib.answers.update(mla_cache_compact=0, mla_pages_resize=-6)
+    with pytest.raises(mla.MlaError):
+        s.commit()
+    lib.answers.clear()
+    lib.calls.clear()
+    s.commit()
+    assert lib.calls == ["mla_pages_resize"]  # the rows were moved already
+    s.attend(**attend)
