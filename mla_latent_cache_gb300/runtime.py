@@ -226,11 +226,13 @@ class SpecStep:
     ``set_tree`` -> ``attend`` (pages for the nodes' rows, norms + rotation + append,
     absorption, tree attention, un-absorption), then ``accept`` (verification against the
     target's probabilities) and ``commit`` (accepted rows moved together, the other pages
-    given back), in this order; ``fork`` between steps.  Everything runs on the device
-    without a host synchronisation, so a step can be captured in a CUDA graph; ``check``
-    raises what the device reported.  A sequence whose nodes get no pages (no free block, or
-    past its table) is reported and sits the step out: outputs 0, accept_len 0, its rows as
-    they were.  Arguments that do not fit raise ValueError before anything is launched.
+    given back), in this order; ``fork`` between steps.  attend, accept, commit and fork run on
+    the device without a host synchronisation, so that they can be captured in a CUDA graph;
+    set_tree copies from the host.  ``check`` raises what the device reported: the last step's
+    attention, and everything else since the last check.  A sequence whose nodes get no pages
+    (no free block, or past its table) is reported and sits the step out: outputs 0,
+    accept_len 0, its rows as they were.  Arguments that do not fit raise ValueError before
+    anything is launched.
     ``stream`` (a torch stream or its handle; None: torch's current one) is the same for every
     call of a step, and for the calls between steps.
     """
@@ -321,8 +323,10 @@ class SpecStep:
         self._stage = after
 
     def set_tree(self, parents: np.ndarray, node_lens: np.ndarray, stream=None):
-        """The step's trees (host arrays): parents [B, T], node_lens [B] (the first node_lens[b] nodes count,
-        the other parents are not looked at)."""
+        """The next step's trees (host arrays): parents [B, T], node_lens [B] (the first node_lens[b] nodes count,
+        the other parents are not looked at).  Copied from the host: waits for the stream."""
+        if self._stage != "attend":
+            raise RuntimeError("set_tree within a step")
         parents, node_lens = np.asarray(parents), np.asarray(node_lens)
         if parents.shape != (self.B, self.T) or node_lens.shape != (self.B,):
             raise ValueError(f"parents {parents.shape}, node_lens {node_lens.shape}")

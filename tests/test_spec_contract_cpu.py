@@ -204,3 +204,19 @@ def test_failed_accept_and_commit_can_be_repeated(step, lib, mla):
     s.commit()
     assert lib.calls == ["mla_pages_resize"]  # the rows were moved already
     s.attend(**attend)
+
+
+def test_trees_are_set_between_steps(step, lib):
+    """The verification goes by the trees that were attended."""
+    s = step(lens=[70, 5])
+    attend, accept = _inputs(s)
+    chain, star = np.tile(np.arange(-1, 3), (2, 1)), np.array([[-1, 0, 0, 0]] * 2)
+    s.set_tree(chain, np.array([4, 4]))
+    for part in (lambda: s.attend(**attend), lambda: s.accept(**accept)):
+        part()
+        with pytest.raises(RuntimeError):
+            s.set_tree(star, np.array([4, 4]))
+        assert s.parents.tolist() == chain.tolist()
+    s.commit()
+    s.set_tree(star, np.array([4, 4]))
+    assert s.parents.tolist() == star.tolist()
