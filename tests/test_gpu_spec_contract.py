@@ -2,6 +2,9 @@
 import numpy as np
 import pytest
 
+from oracle import mla_oracle as M
+from oracle import spec_oracle as O
+from tests._tol import parity
 from tests.test_gpu_spec_step import Harness
 from tests.test_gpu_tree import Tree
 
@@ -133,3 +136,38 @@ def test_steps_on_a_stream_of_their_own(mla, cuda, fp8, handle):
         del busy
     _counts(s)
     assert max(len(r) for r in h.rows) > 6
+
+
+@pytest.mark.parametrize("B,H,T", [(3, 32, 9), (3, 16, 7), (2, 128, 20)])
+def test_attention_of_fp8_steps(mla, cuda, B, H, T):
+    """A step over FP8 rows attends to the rows that the cache holds, pages converted ahead (T H > 128) or by group."""
+    import torch
+    h = Harness(torch, cuda, B, H, T, 64, fp8=True, seed=T)
+    s = h.s
+    f = lambda t: t.float().cpu().numpy().astype(np.float64)  # noqa: E731
+    for step in range(5):
+        h.draw_inputs(tree=step % 2 == 0)
+        base = s.seq_lens.tolist()
+        s.attend(h.q, h.kv, h.cs, *h.w, kv_weight=h.kvw)
+        torch.cuda.synchronize()
+        see = O.ancestors(h.par)
+        o, lse = f(s.o), s.lse.cpu().numpy().astype(np.float64)
+        for b in range(B):
+            n = int(h.n[b])
+            qn, qp, _ = O.rope_append_ref(f(h.q[b]), f(h.kv[b]), None, f(h.kvw), 1e-6, h.table.astype(np.float64),
+                                          base[b] + see[b].sum(-1) - 1, s.interleaved)
+            hist = h.values(h.cached(b, range(base[b] + n)))
+            assert np.array_equal(hist[:base[b]], h.rows[b])
+            k = np.einsum("jc,hnc->hjn", hist[:, :512], f(h.w[0]))
+            v = np.einsum("jc,hvc->hjv", hist[:, :512], f(h.w[1]))
+            x = (np.einsum("thn,hjn->thj", qn[:n], k) + np.einsum("thr,jr->thj", qp[:n], hist[:, 512:])) * M.SCALE
+            x = np.where(O.tree_visible(base[b] + n, n, see[b])[:n, None], x, -np.inf)
+            m = x.max(-1, keepdims=True)
+            e = np.exp(x - m)
+            total = e.sum(-1, keepdims=True)
+            # (the bf16 step's tolerances: from the cached rows on, the arithmetic is the same)
+            parity(o[b, :n], np.einsum("thj,hjv->thv", e / total, v), f"o {b}", mean_rel=8e-3)
+            parity(lse[b, :n], (m + np.log(total))[..., 0], f"lse {b}")
+        s.accept(h.p, h.d, h.tokens, h.ua, h.us, h.V)
+        s.commit()
+        h.check()
