@@ -7,6 +7,7 @@ from oracle import spec_oracle as O
 from tests._tol import parity
 from tests.test_gpu_spec_step import Harness
 from tests.test_gpu_tree import Tree
+from tests.test_gpu_verify import _random
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
 
@@ -171,3 +172,21 @@ def test_attention_of_fp8_steps(mla, cuda, B, H, T):
         s.accept(h.p, h.d, h.tokens, h.ua, h.us, h.V)
         s.commit()
         h.check()
+
+
+def test_verify_replays_give_what_the_eager_call_gave(mla, cuda):
+    import torch
+    r = _random(mla, torch, 8, 6, 5000, torch.float32, True, True, 1)
+    r.check()
+    first = [x.copy() for x in r.results()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        assert r.call() == mla.MLA_OK
+    for x in r.out:
+        x.fill_(-7)
+    g.replay()
+    assert all(np.array_equal(x, y) for x, y in zip(r.results(), first))
+    r.args[3].copy_(torch.rand(8, 6, device="cuda"))
+    r.args[4].copy_(torch.rand(8, device="cuda"))
+    g.replay()
+    r.check()
