@@ -144,14 +144,22 @@ def _ptr(t) -> int | None:
         return t
 
 
+def _stream_getter(torch):
+    """A function for the handle of torch's current stream (of the current device)."""
+    # torch.cuda.current_stream().cuda_stream without the Stream object (0.2 us instead of 3), by names that
+    # torch does not document: where they are missing, by the documented ones
+    device, raw = (getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+    if device is None or raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
 def _torch_stream() -> int:
     """The handle of torch's current stream (of the current device)."""
     global _torch_stream
     import torch
     torch.cuda.init()
-    device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    # (torch.cuda.current_stream().cuda_stream without the Stream object: 0.2 us instead of 3)
-    _torch_stream = lambda: raw(device())  # noqa: E731
+    _torch_stream = _stream_getter(torch)
     return _torch_stream()
 
 

@@ -220,3 +220,12 @@ def test_trees_are_set_between_steps(step, lib):
     s.commit()
     s.set_tree(star, np.array([4, 4]))
     assert s.parents.tolist() == star.tolist()
+
+
+def test_current_stream_with_and_without_torchs_own_names(mla):
+    from types import SimpleNamespace as N
+    cuda = N(current_stream=lambda: N(cuda_stream=7))
+    own = {"_cuda_getDevice": lambda: 3, "_cuda_getCurrentRawStream": lambda device: 10 + device}
+    assert mla._stream_getter(N(_C=N(**own), cuda=cuda))() == 13
+    for missing in own:
+        assert mla._stream_getter(N(_C=N(**{k: v for k, v in own.items() if k != missing}), cuda=cuda))() == 7
