@@ -440,6 +440,8 @@ class SpecStep:
         n = src.numel()
         self._fits("src", src, (self.torch.int32,), (n,))
         self._fits("dst", dst, (self.torch.int32,), (n,))
+        if n > 4096:
+            raise ValueError(f"{n} forks")
         if self._stage != "attend":
             raise RuntimeError("fork within a step")
         with self._on(stream):

@@ -229,3 +229,14 @@ def test_current_stream_with_and_without_torchs_own_names(mla):
     assert mla._stream_getter(N(_C=N(**own), cuda=cuda))() == 13
     for missing in own:
         assert mla._stream_getter(N(_C=N(**{k: v for k, v in own.items() if k != missing}), cuda=cuda))() == 7
+
+
+def test_more_forks_than_a_call_takes(step, lib):
+    """Refused before anything is given back."""
+    s = step(lens=[70, 130], B=2)
+    before = _pages(s)
+    with pytest.raises(ValueError):
+        s.fork(torch.zeros(4097, dtype=torch.int32), torch.ones(4097, dtype=torch.int32))
+    assert lib.calls == [] and _pages(s) == before
+    s.fork(torch.zeros(0, dtype=torch.int32), torch.zeros(0, dtype=torch.int32))
+    assert _pages(s) == before
