@@ -268,7 +268,7 @@ mla_status mla_decode_sparse(const mla_geom* geom, const mla_batch* batch, const
  * counts change; the mask is the decode's alone.  checked, the status word and every
  * other argument as for mla_decode and mla_decode_fp8.
  * mla_decode_tree_fp8 given mla_tree_fp8_workspace_size() bytes (0 on invalid
- * arguments; as much as the batch's longest table as bf16 rows on top of the plan's)
+ * arguments; B * max_pages pages of bf16 rows, 73,728 bytes each, on top of the plan's)
  * converts each page once, ahead of the attention, where a sequence has more than 128
  * query rows (T * H > 128): about twice as fast as with mla_workspace_size() bytes,
  * with which every 128 rows convert the pages they read.

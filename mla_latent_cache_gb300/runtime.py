@@ -233,12 +233,15 @@ class SpecStep:
     (no free block, or past its table) is reported and sits the step out: outputs 0,
     accept_len 0, its rows as they were.  Arguments that do not fit raise ValueError before
     anything is launched.
+    FP8 pages are converted ahead of the attention where T * H > 128, in a workspace of
+    B * max_pages bf16 pages (72 KB each, however many are in use); convert_ahead=False does
+    without it, at about half the speed.
     ``stream`` (a torch stream or its handle; None: torch's current one) is the same for every
     call of a step, and for the calls between steps.
     """
 
     def __init__(self, B: int, H: int, T: int, max_pages: int, num_blocks: int, device="cuda",
-                 cache_format: str = "bf16", interleaved: bool = True, num_slots: int = 0):
+                 cache_format: str = "bf16", interleaved: bool = True, num_slots: int = 0, convert_ahead: bool = True):
         import torch
         self.torch = torch
         dev = torch.device(device)
@@ -254,7 +257,8 @@ class SpecStep:
         self.cache_format = cache_format
         if cache_format == "fp8":
             self.pool = torch.zeros((num_blocks, 64, 656), dtype=torch.uint8, device=dev)
-            self.ws_bytes = L.mla_tree_fp8_workspace_size(self.geom, self.batch)
+            size = L.mla_tree_fp8_workspace_size if convert_ahead else L.mla_workspace_size
+            self.ws_bytes = size(self.geom, self.batch)
         else:
             self.pool = torch.zeros((num_blocks, 64, 576), dtype=torch.bfloat16, device=dev)
             self.cache = L.cache_from_pool(self.pool)

@@ -174,6 +174,21 @@ def test_attention_of_fp8_steps(mla, cuda, B, H, T):
         h.check()
 
 
+def test_fp8_steps_without_room_for_converted_pages(mla, cuda):
+    """The same bits, step after step."""
+    import torch
+    from mla_latent_cache_gb300.runtime import SpecStep
+    a, b = (Harness(torch, cuda, 2, 32, 9, 64, fp8=True, seed=5) for _ in range(2))
+    b.s = SpecStep(2, 32, 9, max_pages=8, num_blocks=16, device=cuda, cache_format="fp8", convert_ahead=False)
+    assert b.s.ws_bytes < a.s.ws_bytes
+    for step in range(6):
+        for h in (a, b):
+            h.draw_inputs(tree=step % 2 == 0)
+            h.device_step()
+            h.check()
+        assert torch.equal(a.s.o, b.s.o) and torch.equal(a.s.lse, b.s.lse) and torch.equal(a.s.pool, b.s.pool)
+
+
 def test_verify_replays_give_what_the_eager_call_gave(mla, cuda):
     import torch
     r = _random(mla, torch, 8, 6, 5000, torch.float32, True, True, 1)

@@ -240,3 +240,11 @@ def test_more_forks_than_a_call_takes(step, lib):
     assert lib.calls == [] and _pages(s) == before
     s.fork(torch.zeros(0, dtype=torch.int32), torch.zeros(0, dtype=torch.int32))
     assert _pages(s) == before
+
+
+def test_the_workspace_for_converted_pages_can_be_declined(lib, mla):
+    from mla_latent_cache_gb300.runtime import SpecStep
+    size = lambda **kw: SpecStep(3, 32, 9, max_pages=5, num_blocks=8, device="cpu", cache_format="fp8", num_slots=4, **kw).ws_bytes  # noqa: E731
+    plan = mla.mla_workspace_size(mla.make_geom(32), mla.make_batch(3, 9, False, 5, 4))
+    assert size(convert_ahead=False) == plan
+    assert plan + 15 * 64 * 1152 <= size() <= plan + 15 * 64 * 1152 + 512
