@@ -73,7 +73,7 @@ typedef struct CUstream_st* mla_stream_t;
 typedef enum {
   MLA_OK = 0,
   MLA_ERR_ARG = -1,          /* null pointer, negative size, unsupported flag; memory of another device than
-                                the current one (the calls of a speculative step) */
+                                the current one (the calls of a speculative step, by one of their arrays) */
   MLA_ERR_SHAPE = -2,        /* geometry not supported (d_* must be 512/64/128/128, P = 64, 1 <= H <= 128, 128 % H == 0) */
   MLA_ERR_ALIGN = -3,        /* pointer or stride not 16-byte (outputs: 32-byte) aligned */
   MLA_ERR_WORKSPACE = -4,    /* workspace smaller than mla_workspace_size() */
@@ -486,7 +486,9 @@ mla_status mla_rope_append_fp8(const mla_geom* geom, int N, const void* q, int64
  *     probabilities of the token after node t, and those that node t's children were
  *     drawn from (independent draws; not read at nodes without children).  draft_probs
  *     NULL: each draft is taken as certain (a point mass), as the likeliest tokens of a
- *     drafter are.  Negative values, infinities and NaN count as 0; rows need not sum to 1 exactly.
+ *     drafter are.  Negative values, infinities and NaN count as 0; rows need not sum to 1
+ *     (the rule below is as it stands), but to less than 2^31: past that, products leave
+ *     fp32's range, and which nodes and token are chosen is not specified.
  *   u_accept float32 [B, T] (node t's number), u_sample float32 [B]: in [0, 1).
  * Rule: from cur = 0, the children of cur are tried in index order.  With p, q the rows
  * of cur, k of its children refused so far, R_k = max(p - C_k q, 0), C_0 = 0, Z_0 = 1,

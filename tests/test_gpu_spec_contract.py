@@ -189,6 +189,19 @@ def test_fp8_steps_without_room_for_converted_pages(mla, cuda):
         assert torch.equal(a.s.o, b.s.o) and torch.equal(a.s.lse, b.s.lse) and torch.equal(a.s.pool, b.s.pool)
 
 
+@pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("power", [-60, 30])
+def test_verify_rows_far_from_a_sum_of_one(mla, cuda, power, draft):
+    """Rows whose values sum to 2^-60 and to 2^30 decide by the rule as it stands (a first test's mass is 1)."""
+    import torch
+    r = _random(mla, torch, 24, 9, 3001, torch.float32, draft, True, 2, sharp=1.0, noise=2.0)
+    r.p *= 2.0 ** power
+    if draft:
+        r.q *= 2.0 ** power
+    assert r.call() == mla.MLA_OK
+    r.check()
+
+
 def test_verify_replays_give_what_the_eager_call_gave(mla, cuda):
     import torch
     r = _random(mla, torch, 8, 6, 5000, torch.float32, True, True, 1)
