@@ -343,7 +343,10 @@ class SpecStep:
                 dst.copy_(self.torch.from_numpy(np.ascontiguousarray(src, dtype=np.int32)))
 
     def attend(self, q, kv, cos_sin, w_uk, w_uv, q_weight=None, kv_weight=None, eps: float = 1e-6, stream=None):
-        """The nodes' rows into the cache and their attention: q [B, T, H, 192], kv [B, T, 576] -> o [B, T, H, 128]."""
+        """The nodes' rows into the cache and their attention: q [B, T, H, 192], kv [B, T, 576] -> o [B, T, H, 128].
+
+        cos_sin [positions, 64] covers every position: a node past it is reported, its row is not written, and
+        what the step gives for its sequence is not to be used."""
         torch, bt = self.torch, self.block_table
         B, T, H, N = self.B, self.T, self.H, self.B * self.T
         bf16, f32 = (torch.bfloat16,), (torch.float32,)
