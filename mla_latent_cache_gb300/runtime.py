@@ -307,24 +307,20 @@ class SpecStep:
         """Torch's part of a call goes to the stream that the library's calls take (None: the current one of
         the step's device), and what it allocates belongs to that stream."""
         torch = self.torch
+        if self.device.type != "cuda" or (stream is None and torch.cuda.current_device() == self.device.index):
+            return contextlib.nullcontext()
         on = contextlib.ExitStack()
-        if self.device.type == "cuda":
-            if torch.cuda.current_device() != self.device.index:
-                on.enter_context(torch.cuda.device(self.device))
-            if stream is not None:
-                if isinstance(stream, int):
-                    stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-                on.enter_context(torch.cuda.stream(stream))
+        on.enter_context(torch.cuda.device(self.device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            on.enter_context(torch.cuda.stream(stream))
         return on
 
-    @contextlib.contextmanager
-    def _part(self, stage, after, stream):
-        """One part of the step, on `stream`; what fails leaves the step where it was."""
+    def _expect(self, stage):
+        """The part that is next (it becomes another one when a part is through: what fails leaves the step where it was)."""
         if self._stage != stage:
             raise RuntimeError(f"{stage} where {self._stage} is next")
-        with self._on(stream):
-            yield
-        self._stage = after
 
     def set_tree(self, parents: np.ndarray, node_lens: np.ndarray, stream=None):
         """The next step's trees (host arrays): parents [B, T], node_lens [B] (the first node_lens[b] nodes count,
@@ -359,40 +355,44 @@ class SpecStep:
                                ("kv_weight", kv_weight, (512,))):
             if t is not None:
                 self._fits(name, t, bf16, shape)
-        with self._part("attend", "accept", stream), contextlib.ExitStack() as undo:
+        self._expect("attend")
+        with self._on(stream):
             torch.add(self.seq_lens, self.node_lens, out=self.new_lens)
             L.check(L.mla_pages_resize(self.refs, self.num_blocks, bt, self.max_pages, self.max_pages, self.seq_lens,
                                        self.new_lens, self.B, self.held_lens, stream), "mla_pages_resize")
-            undo.callback(L.mla_pages_resize, self.refs, self.num_blocks, bt, self.max_pages, self.max_pages,
-                          self.held_lens, self.seq_lens, self.B, self.new_lens, stream)
-            granted = self.held_lens == self.new_lens
-            torch.mul(self.node_lens, granted, out=self.live)
-            torch.add(self.seq_lens, self.live, out=self.tree_lens)
-            row = self.seq_lens[:, None] + self.nodes
-            blk = bt.gather(1, (row // 64).clamp(max=self.max_pages - 1).long())
-            counts = self.nodes < self.live[:, None]
-            slots = torch.where(counts & (blk >= 0), blk * 64 + row % 64, -1).int()
-            positions = torch.where(counts, self.seq_lens[:, None] + self.depth, 0).int()
-            args = (self.geom, N, q, q_step, q.stride(2) if H > 1 else 192, kv, kv_step, q_weight, kv_weight, eps, cos_sin,
-                    cos_sin.shape[0], positions, self.interleaved)
-            tail = (slots, self.q_nope, self.q_pe, stream)
-            if self.cache_format == "fp8":
-                L.check(L.mla_rope_append_fp8(*args, self.pool, self.num_blocks, *tail), "mla_rope_append_fp8")
-            else:
-                L.check(L.mla_rope_append(*args, self.cache, *tail), "mla_rope_append")
-            L.check(L.mla_absorb_q(self.geom, self.q_nope, w_uk, self.q_lat, N, stream), "mla_absorb_q")
-            L.check(L.mla_plan_tree(self.geom, self.batch, self.tree_lens, self.live, self.workspace, self.ws_bytes,
-                                    stream), "mla_plan_tree")
-            tail = (bt, self.max_pages, self.tree_lens, self.live, self.mask, 0, self.o_lat, self.lse, self.workspace,
-                    self.ws_bytes, stream)
-            if self.cache_format == "fp8":
-                L.check(L.mla_decode_tree_fp8(self.geom, self.batch, self.q_lat, self.q_pe, self.pool, self.num_blocks,
-                                              *tail), "mla_decode_tree_fp8")
-            else:
-                L.check(L.mla_decode_tree(self.geom, self.batch, self.q_lat, self.q_pe, self.cache, *tail),
-                        "mla_decode_tree")
-            L.check(L.mla_unabsorb_o(self.geom, self.o_lat, w_uv, self.o, N, stream), "mla_unabsorb_o")
-            undo.pop_all()
+            try:
+                granted = self.held_lens == self.new_lens
+                torch.mul(self.node_lens, granted, out=self.live)
+                torch.add(self.seq_lens, self.live, out=self.tree_lens)
+                row = self.seq_lens[:, None] + self.nodes
+                blk = bt.gather(1, (row // 64).clamp(max=self.max_pages - 1).long())
+                counts = self.nodes < self.live[:, None]
+                slots = torch.where(counts & (blk >= 0), blk * 64 + row % 64, -1).int()
+                positions = torch.where(counts, self.seq_lens[:, None] + self.depth, 0).int()
+                args = (self.geom, N, q, q_step, q.stride(2) if H > 1 else 192, kv, kv_step, q_weight, kv_weight, eps, cos_sin,
+                        cos_sin.shape[0], positions, self.interleaved)
+                tail = (slots, self.q_nope, self.q_pe, stream)
+                if self.cache_format == "fp8":
+                    L.check(L.mla_rope_append_fp8(*args, self.pool, self.num_blocks, *tail), "mla_rope_append_fp8")
+                else:
+                    L.check(L.mla_rope_append(*args, self.cache, *tail), "mla_rope_append")
+                L.check(L.mla_absorb_q(self.geom, self.q_nope, w_uk, self.q_lat, N, stream), "mla_absorb_q")
+                L.check(L.mla_plan_tree(self.geom, self.batch, self.tree_lens, self.live, self.workspace, self.ws_bytes,
+                                        stream), "mla_plan_tree")
+                tail = (bt, self.max_pages, self.tree_lens, self.live, self.mask, 0, self.o_lat, self.lse, self.workspace,
+                        self.ws_bytes, stream)
+                if self.cache_format == "fp8":
+                    L.check(L.mla_decode_tree_fp8(self.geom, self.batch, self.q_lat, self.q_pe, self.pool, self.num_blocks,
+                                                  *tail), "mla_decode_tree_fp8")
+                else:
+                    L.check(L.mla_decode_tree(self.geom, self.batch, self.q_lat, self.q_pe, self.cache, *tail),
+                            "mla_decode_tree")
+                L.check(L.mla_unabsorb_o(self.geom, self.o_lat, w_uv, self.o, N, stream), "mla_unabsorb_o")
+            except BaseException:    # the pages are given back
+                L.mla_pages_resize(self.refs, self.num_blocks, bt, self.max_pages, self.max_pages, self.held_lens,
+                                   self.seq_lens, self.B, self.new_lens, stream)
+                raise
+        self._stage = "accept"
         return self.o
 
     def accept(self, target_probs, draft_probs, tokens, u_accept, u_sample, V: int, stream=None):
@@ -408,15 +408,18 @@ class SpecStep:
         self._fits("tokens", tokens, (torch.int32,), (B, T))
         self._fits("u_accept", u_accept, (torch.float32,), (B, T))
         self._fits("u_sample", u_sample, (torch.float32,), (B,))
-        with self._part("accept", "commit", stream):
+        self._expect("accept")
+        with self._on(stream):
             L.check(L.mla_verify_tree(B, T, V, target_probs, draft_probs, dtype, step, tokens, self.parents, self.live,
                                       u_accept, u_sample, self.accept_len, self.accept_idx, self.out_tokens, stream),
                     "mla_verify_tree")
+        self._stage = "commit"
         return self.accept_len, self.out_tokens
 
     def commit(self, stream=None):
         """The accepted nodes' rows become the sequences' own; the other pages are given back."""
-        with self._part("commit", "attend", stream):
+        self._expect("commit")
+        with self._on(stream):
             if not self._moved:       # (moving the rows twice would mix them)
                 args = (self.block_table, self.max_pages, self.max_pages, self.tree_lens, self.live, self.accept_len,
                         self.accept_idx, self.B, self.T, self.new_lens, stream)
@@ -428,6 +431,7 @@ class SpecStep:
             L.check(L.mla_pages_resize(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
                                        self.held_lens, self.new_lens, self.B, self.seq_lens, stream), "mla_pages_resize")
             self._moved = False
+        self._stage = "attend"
 
     def _released(self, src, dst):
         """Boolean [B]: the sequences that become another's fork, by the rules of mla_pages_fork."""
