@@ -4,10 +4,12 @@
 // at ~2.3 us per page and CTA pair (its converter warps are the bound) against ~0.95 us
 // for a bf16 page.  Where a sequence has more than one group (trees: one per node at 128
 // heads), every group would convert the same pages again; converting each page once into
-// a scratch pool costs its bytes (656 read and 1152 written per row, bound by memory) and
-// lets the groups read bf16 pages from the L2.  24 trees of up to 11 nodes x 128 heads
-// over 256 .. 4096 rows: 220 us converted by group, 134 us ahead.  The values are the
-// same: E4M3(code) * scale in fp32, rounded to bf16.
+// a scratch pool costs 656 bytes read and 1152 written per row and lets the groups read
+// bf16 pages from the L2.  24 trees of up to 11 nodes x 128 heads over 256 .. 4096 rows:
+// 220 us converted by group, 136 us ahead, of which the conversion takes 14 (9 for its bytes
+// at the copy rate: a sequence has as many CTAs whatever its length, so that those of the
+// long ones take three turns).  The values are the same: E4M3(code) * scale in fp32, rounded
+// to bf16.
 //
 // Page p of sequence b becomes block b * max_pages + p of the scratch pool, and the
 // scratch block table says so.  A warp takes a row at a time: lane l converts codes
