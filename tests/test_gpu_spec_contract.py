@@ -99,6 +99,30 @@ def test_a_sequence_forked_from_itself(mla, cuda, fmt):
     _counts(s)
 
 
+def test_forks_captured_and_replayed(mla, cuda):
+    """A captured fork takes the numbers that its arrays hold when it is replayed, refused ones among them."""
+    import torch
+    s = _committed(torch, cuda, [70, 130, 5, 64], 4)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda)  # noqa: E731
+    src, dst = i32([-1, -1]), i32([-1, -1])
+    s.fork(src, dst)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.fork(src, dst)
+    for a, b in (([0, 0], [1, 9]), ([1, 2], [3, 3]), ([2, 2], [0, 2]), ([0, 0], [1, 3])):
+        before = _held(s)
+        src.copy_(i32(a))
+        dst.copy_(i32(b))
+        g.replay()
+        torch.cuda.synchronize()
+        after = _held(s)
+        for k in range(4):
+            f = [x for x, y in zip(a, b) if y == k and b.count(k) == 1 and x not in b]
+            assert (after[k][0], after[k][2]) == (before[f[0]][0], before[f[0]][2]) if f else after[k] == before[k]
+        _counts(s)
+    assert mla.mla_read_device_status(None)[0] == mla.MLA_ERR_DEVICE_CHECK
+
+
 @pytest.mark.parametrize("handle", [False, True])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_steps_on_a_stream_of_their_own(mla, cuda, fp8, handle):
