@@ -53,6 +53,10 @@ constexpr int kTable = 1024;          // 2^(-j / 1024)
 constexpr int kPerOctave = 64;        // buckets
 constexpr int kOctaves = 46;
 constexpr int kBuckets = kOctaves * kPerOctave;
+// Buckets that can hold a mass: places are rounded to nearest, so that the first half place of bucket 45
+// * 64 lies within 45 octaves, where a mass is just above 2^-45 and becomes one unit of 2^-44; the next
+// bucket begins 15.5 places past them, at 0.495 units, which become none.
+constexpr int kMassBuckets = (kMassBits + 1) * kPerOctave + 1;
 constexpr float kFloorOctaves = 45.5f;   // what is further off has no mass (less than half of 2^-44)
 constexpr int kList = 1024;           // tokens that one CTA sorts
 constexpr int kGroup = 8;             // tokens a thread takes at once
@@ -799,7 +803,7 @@ __device__ __noinline__ void bucket_masses(bool cleared, bool counts) {
       constexpr uint32_t kBase = 4 * (kMagicBits / (kTable / kPerOctave));
 #pragma unroll
       for (int e = 0; e < 4; ++e)       // (what has no mass goes to the lane's own place, not all of it to one)
-        add_mass(at[e] < kBase + 4 * (kBuckets - kPerOctave) ? limbs - kBase + at[e] : limbs + 4 * (threadIdx.x & 31), m[e]);
+        add_mass(at[e] < kBase + 4 * kMassBuckets ? limbs - kBase + at[e] : limbs + 4 * (threadIdx.x & 31), m[e]);
       if (counts) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
