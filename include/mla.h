@@ -564,7 +564,7 @@ mla_status mla_verify_tree(int B, int T, int V, const void* target_probs, const 
  * temperature, min-p, top-k and top-p, or the probabilities that these leave (as
  * mla_verify_tree takes them: target_probs and draft_probs), or both.
  *   logits: row r at base + r * row_stride elements (fp32 or bf16 by dtype; row_stride >= V,
- *     rows 16-byte aligned), 1 <= V <= 2^20.  -inf and NaN: a token that is out (masked).
+ *     rows 16-byte aligned), 1 <= V < 2^20.  -inf and NaN: a token that is out (masked).
  *   temperature float32 [N] (NULL: 1), >= 0, 0 the likeliest token alone; top_k int32 [N]
  *     (NULL, or <= 0: off); top_p float32 [N] (NULL, >= 1 or NaN: off); min_p float32 [N]
  *     (NULL, <= 0 or NaN: off; above 1 as 1); u float32 [N] in [0, 1) (numbers outside

@@ -210,7 +210,7 @@ cudaError_t launch_pages_fork(int32_t* refs, int num_blocks, int32_t* block_tabl
 cudaError_t launch_cache_copy(const CacheView& cv, unsigned char* rows_fp8, const int32_t* copies, int n,
                               cudaStream_t st);
 // Sampling (mla_sample): logits, and probabilities where they are wanted, bf16 or fp32.
-constexpr int kMaxSampleTokens = 1 << 20;       // masses are sums of multiples of 2^-44, in 64 bits
+constexpr int kMaxSampleTokens = (1 << 20) - 1; // sums of masses of up to 2^44 units, in 64 bits (2^20 equal logits: 2^64)
 struct SampleCall {
   int N, V;
   const void* logits;

@@ -613,7 +613,7 @@ class ServeStep(_PagedLayer):
                 raise ValueError(f"{name}: strides {t.stride()} at {t.data_ptr() % 16}")
             return step
 
-        if V > 1 << 20 or (u is None and probs is None):
+        if V >= 1 << 20 or (u is None and probs is None):
             raise ValueError(f"V {V}, u {u}, probs {probs}")
         step = rows("logits", logits)
         probs_step = 0 if probs is None else rows("probs", probs)

@@ -104,3 +104,12 @@ def test_shared_refusals(mla):
     assert bf16(cache=_cache(mla, ckv=0x1002)) == mla.MLA_ERR_ALIGN
     assert fp8(rows=None) == mla.MLA_ERR_ARG and fp8(nb=0) == mla.MLA_ERR_ARG
     assert fp8(rows=0x80008) == mla.MLA_ERR_ALIGN and fp8(nb=1 << 25) == mla.MLA_ERR_SHAPE
+
+
+def test_sample_vocabularies_whose_sums_do_not_fit(mla):
+    """2^20 equal logits have a mass of 2^44 units each, together 2^64: one more than the sums hold."""
+    names = ["N", "V", "logits", "dtype", "stride", "temp", "k", "p", "mp", "u", "tokens", "probs", "pd", "ps"]
+    call = _caller(mla.mla_sample, names, dict(N=0, V=1 << 20, logits=0x10000, dtype=mla.MLA_DTYPE_F32, stride=1 << 20, temp=None,
+                                               k=None, p=None, mp=None, u=0x60000, tokens=0x70000, probs=None, pd=0, ps=0))
+    assert call() == mla.MLA_ERR_SHAPE and call(N=2) == mla.MLA_ERR_SHAPE
+    assert call(V=(1 << 20) - 1) == mla.MLA_OK

@@ -151,3 +151,13 @@ def test_sharing_and_sampling_arguments(step, lib):
     args = lib.args["mla_sample"]
     assert args[3] == 0 and args[9:14] == (None, None, p, 0, 104)
     assert s.sample(torch.zeros(3, 104), 101, u=torch.zeros(3)) is s.tokens
+
+
+def test_a_vocabulary_past_the_samplings_sums(step, lib):
+    s = step(B=1)
+    x = torch.zeros(1, 1 << 20)
+    with pytest.raises(ValueError):
+        s.sample(x, 1 << 20, u=torch.zeros(1))
+    assert lib.calls == []
+    s.sample(x, (1 << 20) - 1, u=torch.zeros(1))
+    assert lib.args["mla_sample"][1] == (1 << 20) - 1
