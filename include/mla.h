@@ -568,7 +568,7 @@ mla_status mla_verify_tree(int B, int T, int V, const void* target_probs, const 
  *   temperature float32 [N] (NULL: 1), >= 0, 0 the likeliest token alone; top_k int32 [N]
  *     (NULL, or <= 0: off); top_p float32 [N] (NULL, >= 1 or NaN: off); min_p float32 [N]
  *     (NULL, <= 0 or NaN: off; above 1 as 1); u float32 [N] in [0, 1) (numbers outside
- *     count as 0 and as 1 - 2^-24).
+ *     count as 0 and as 1 - 2^-24, NaN as 0).
  * Rule: the tokens stand in order, the larger logit first, the lower index first among
  * equals; e_i = exp((l_i - l_max) / temperature) (1 for l_i = l_max, infinite or not; 0 where
  * the difference passes fp32's range).  Each filter keeps a leading part of what the one

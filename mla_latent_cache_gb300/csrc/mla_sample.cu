@@ -1182,7 +1182,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleCall c, int s
   float mp = c.min_p ? c.min_p[row] : 0.f;
   const int top_k = c.top_k ? c.top_k[row] : 0;
   const float p = c.top_p ? c.top_p[row] : 1.f;
-  const float u = c.tokens ? fminf(c.u[row], 1.f - 0x1p-24f) : 0.f;
+  float u = c.tokens ? c.u[row] : 0.f;
+  u = u >= 1.f ? 1.f - 0x1p-24f : u;                 // (NaN stays, and counts as 0: fraction)
   // What goes by the settings alone, and the buckets' clearing, while the logits are on their way.
   const bool greedy = temp == 0.f;
   constexpr double kLog2e = 1.4426950408889634074;
