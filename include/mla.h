@@ -582,8 +582,8 @@ mla_status mla_verify_tree(int B, int T, int V, const void* target_probs, const 
  * not written.  A row without a token that counts, or with a temperature that is negative or
  * NaN (reported by mla_read_device_status, MLA_ERR_DEVICE_CHECK), gets token -1 and
  * probabilities 0.
- * e_i is held as a multiple of 2^-44 of the largest (for the probabilities as a pair of fp32
- * values, 0 below 2^-60) and summed exactly: results do not depend
+ * e_i is summed as a multiple of 2^-44 of the largest, exactly (for the probabilities, and against
+ * min_p, it is a pair of fp32 values, 0 below 2^-60): results do not depend
  * on how the work is split, and equal arguments give equal results.
  */
 mla_status mla_sample(int N, int V, const void* logits, mla_dtype dtype, int64_t row_stride, const float* temperature,

@@ -138,6 +138,8 @@ __device__ __forceinline__ Term term_of(float l, const Scale& sc, const float2* 
   const float rh = fmaf(Th, zh, Th);
   return {rh, fmaf(Th, zh, Th - rh) + fmaf(Th, rest, fmaf(Tl, zh, Tl)), place};
 }
+// Whether min-p leaves the token out: by the pair, whose mass may be rounded past the bound.
+__device__ __forceinline__ bool below(const Term& x, float min_p) { return (x.hi - min_p) + x.lo < 0.f; }
 // The pair as a multiple of 2^-44, rounded to nearest.
 __device__ __forceinline__ u64 fixed_of(float hi, float lo) {
   const float a = hi + 2.f;                         // units of 2^-22
@@ -251,7 +253,7 @@ struct Row {
   bool carried;              // the slices are of more than kFlush tokens (the same for all CTAs)
   bool infinite;             // the maximum is +inf: those tokens are equal, no others count
   Scale scale;
-  u64 least;                 // min-p: the least mass that counts
+  float min_p;               // 0: off
   float cut;                 // the last token kept so far: logit and index
   int cut_index;
 
@@ -338,11 +340,18 @@ __device__ __noinline__ u64 mass_of(float l) {
   const Term x = term_of(fmaxf(l, sc.floor), sc, sm->table);
   return fixed_of(x.hi, x.lo);
 }
+// Whether min-p leaves it.  (What is past the floor counts as at the floor: a min-p below that leaves it
+// among top-k's, behind all others and without mass, and the probabilities leave it out.)
+__device__ __noinline__ bool min_p_keeps(float l) {
+  const Sm* const sm = state();
+  const Scale sc = sm->row.scale;
+  if (sc.wild && !(octaves_off(l, sc) < kFloorOctaves)) return sm->row.min_p <= 0x1p-45f;
+  return !below(term_of(fmaxf(l, sc.floor), sc, sm->table), sm->row.min_p);
+}
 __device__ __forceinline__ u64 weight_of(float l, int i, bool by_count) {
   const Sm* const sm = state();
-  if (!sm->row.kept(l, i)) return 0;
-  const u64 m = mass_of(l);
-  return m < sm->row.least ? 0 : by_count ? 1 : m;
+  if (!sm->row.kept(l, i) || (sm->row.min_p > 0.f && !min_p_keeps(l))) return 0;
+  return by_count ? 1 : mass_of(l);
 }
 
 // Running sums over the block of two values (the totals, too).
@@ -611,14 +620,14 @@ __device__ __forceinline__ int gather(const Row& r, L like, F want) {
 __device__ __forceinline__ uint32_t entry_key(u64 e) { return (uint32_t)(e >> 32); }
 __device__ __forceinline__ int entry_index(u64 e) { return (int)~(uint32_t)e; }
 
-// The list in the tokens' order, and their running masses (0 for what is below min-p's).
+// The list in the tokens' order, and their running masses (0 for what min-p leaves out).
 __device__ __noinline__ void sort_list(int n) {
   Sm* const sm = state();
   const int tid = threadIdx.x;
-  const u64 least = sm->row.least;
+  const bool by_min_p = sm->row.min_p > 0.f;
   auto mass_at = [&](int i) {
-    const u64 m = mass_of(value_of(entry_key(sm->list[i])));
-    return m < least ? 0 : m;
+    const float l = value_of(entry_key(sm->list[i]));
+    return by_min_p && !min_p_keeps(l) ? 0 : mass_of(l);
   };
   __syncthreads();
   if (n <= kThreads / 4) {
@@ -762,8 +771,8 @@ __device__ __forceinline__ void tell_border(const Border& b) {
   for (int k = 0; k < sm->row.size; ++k) in_cta(sm, k)->border = b;
 }
 
-// Counts and masses of the buckets (masses not below min-p's).
-template <typename T>
+// Counts and masses of the buckets (of tokens that min-p leaves: kMinP where it is on).
+template <typename T, bool kMinP>
 __device__ __noinline__ void bucket_masses(bool cleared, bool counts) {
   Sm* const sm = state();
   const Row r = sm->row;
@@ -775,9 +784,9 @@ __device__ __noinline__ void bucket_masses(bool cleared, bool counts) {
   if (r.scale.wild) {
     histogram<T>(r, [&](const float (&v)[kGroup], int) {
       for (int e = 0; e < kGroup; ++e) {
-        const u64 m = v[e] > -INFINITY ? mass_of(v[e]) : 0;
-        if (m >= r.least) add_mass(limbs + 4 * bucket_of(v[e], r.scale), m);
-        if (counts && v[e] > -INFINITY && m >= r.least) add_shared<0>(counts_at + 4 * bucket_of(v[e], r.scale), 1);
+        if (!(v[e] > -INFINITY) || (kMinP && !min_p_keeps(v[e]))) continue;
+        add_mass(limbs + 4 * bucket_of(v[e], r.scale), mass_of(v[e]));
+        if (counts) add_shared<0>(counts_at + 4 * bucket_of(v[e], r.scale), 1);
       }
     });
     share_octaves(true, counts);
@@ -789,16 +798,14 @@ __device__ __noinline__ void bucket_masses(bool cleared, bool counts) {
     for (int e0 = 0; e0 < kGroup; e0 += 4) {
       u64 m[4];
       uint32_t at[4];
+      bool in[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const Term x = term_of(fmaxf(v[e0 + e], r.scale.floor), r.scale, sm->table);
         m[e] = fixed_of(x.hi, x.lo);
         at[e] = 4 * (x.place / (kTable / kPerOctave));       // + kBase
-      }
-      if (r.least) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (m[e] < r.least) m[e] = 0;
+        in[e] = !kMinP || !below(x, r.min_p);
+        if (kMinP && !in[e]) m[e] = 0;
       }
       constexpr uint32_t kBase = 4 * (kMagicBits / (kTable / kPerOctave));
 #pragma unroll
@@ -806,12 +813,16 @@ __device__ __noinline__ void bucket_masses(bool cleared, bool counts) {
         add_mass(at[e] < kBase + 4 * kMassBuckets ? limbs - kBase + at[e] : limbs + 4 * (threadIdx.x & 31), m[e]);
       if (counts) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          add_shared<0>(counts_at - kBase + at[e], v[e0 + e] > -INFINITY && (m[e] || r.least == 0));
+        for (int e = 0; e < 4; ++e) add_shared<0>(counts_at - kBase + at[e], v[e0 + e] > -INFINITY && in[e]);
       }
     }
   });
   share_octaves(true, counts);
+}
+
+template <typename T>
+__device__ __forceinline__ void row_masses(bool cleared, bool counts) {
+  if (state()->row.min_p > 0.f) bucket_masses<T, true>(cleared, counts); else bucket_masses<T, false>(cleared, counts);
 }
 
 // The token at which the running weight reaches W (the rows of buckets as share_octaves left
@@ -1036,7 +1047,7 @@ __device__ __noinline__ bool few_tokens(float mine, int k, float min_p, float p,
     }
   }
   // (a bucket's bounds are off by half a place, a 32nd of it)
-  if (r.least) last_bucket = min(last_bucket, (int)(-log2f(min_p) * kPerOctave) + 1);
+  if (min_p > 0.f) last_bucket = min(last_bucket, (int)(-log2f(min_p) * kPerOctave) + 1);
   const Range range = range_of(0, last_bucket, r.scale);
   const int n = gather<T>(r, [&](float l) { return range.has(l); },
                           [&](float l, int) { return bucket_of(l, r.scale) <= last_bucket; });
@@ -1045,8 +1056,8 @@ __device__ __noinline__ bool few_tokens(float mine, int k, float min_p, float p,
     sort_list(n);
     const int left = k > 0 ? min(k, n) : n;
     const u64 Z = sm->sum[left - 1];
-    // without top-p, all that min-p leaves, those without mass among them
-    const int last = p < 1.f ? place_in_list(left, reach(p, Z)) : r.least ? place_in_list(left, Z) : left - 1;
+    // (without top-p the list's tokens that min-p leaves out are behind the last one of those left, and add nothing)
+    const int last = p < 1.f ? place_in_list(left, reach(p, Z)) : left - 1;
     const u64 M = sm->sum[last];
     const int at = token ? place_in_list(left, pass(u, M)) : 0;
     if (threadIdx.x == 0) {
@@ -1099,14 +1110,14 @@ __device__ __noinline__ bool both(u64 Z, float p, float u, int32_t* token, bool 
 template <typename T>
 __device__ __noinline__ u64 many(bool cleared, int k, float p, float u, int32_t* token, bool probs) {
   Sm* const sm = state();
-  bucket_masses<T>(cleared, k > 0);
+  row_masses<T>(cleared, k > 0);
   const int rank = sm->row.rank;
   u64 M = sm->omass_run[kOctaves - 1];
   const u64 all = sm->ocount_run[kOctaves - 1];
   if (k > 0 && (u64)k < all) {
     const bool whole = locate<T>((u64)k, true);
     M = take_cut();
-    if (!whole) bucket_masses<T>(false, false);
+    if (!whole) row_masses<T>(false, false);
   }
   bool whole = true;
   if (p < 1.f) {
@@ -1115,7 +1126,7 @@ __device__ __noinline__ u64 many(bool cleared, int k, float p, float u, int32_t*
     M = take_cut();
   }
   if (token) {
-    if (!whole) bucket_masses<T>(false, false);
+    if (!whole) row_masses<T>(false, false);
     locate<T>(pass(u, M), false);
     if (threadIdx.x == 0 && rank == 0) *token = sm->border.index;
   }
@@ -1193,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleCall c, int s
   r.scale.cl = scale.x > 0.f && scale.x < 3.4028234e38f ? scale.y : 0.f;     // (temperatures of 0x1p-128, infinity)
   const float off = kFloorOctaves / r.scale.ch;
   mp = mp > 0.f ? fminf(mp, 1.f) : 0.f;
-  r.least = __float2ull_ru(mp * (float)(1ull << kMassBits));
+  r.min_p = mp;
   const int k = greedy ? 1 : top_k;
   const bool few = few_left(temp, top_k, mp);
   clear_buckets(!few, r.carried && !few);
@@ -1267,13 +1278,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleCall c, int s
       for (int e = 0; e < kGroup; ++e)
         if (!(octaves_off(v[e], sc) < 60.f)) left &= ~(1u << e);
     }
+    if (row_now.min_p > 0.f) {
+#pragma unroll 1
+      for (unsigned x = left; x; x &= x - 1) {
+        const int e = __ffs(x) - 1;
+        if (below(term_of(row_now.clean(entry(static_cast<const T*>(row_now.logits), kGroup * g + e)), sc, sm->table), row_now.min_p))
+          left &= ~(1u << e);
+      }
+    }
     if (left) {
       // e / M rounded once: the pair times 2^44 / M as a pair
 #pragma unroll
       for (int e = 0; e < kGroup; ++e) {
         const Term x = term_of(left >> e & 1u ? v[e] : sc.max, sc, sm->table);
         const float q = fmaf(x.hi, inv.x, fmaf(x.hi, inv.y, x.lo * inv.x));
-        if (row_now.least && fixed_of(x.hi, x.lo) < row_now.least) left &= ~(1u << e);
         out[e] = left >> e & 1u ? q : 0.f;
       }
     }
