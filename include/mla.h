@@ -316,8 +316,8 @@ mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, con
  * take a row per query row of their group; the plan header's MLA_HDR_CAUSAL word is 4 + causal,
  * MLA_HDR_NUM_PARTIALS and MLA_HDR_CAP_PARTIALS count partial rows.  Sets that do not rise or
  * leave the batch, and negative prefixes, are reported (info = B), and nothing is shared.
- * A workspace without such a plan of these sizes is reported (MLA_ERR_PLAN_STALE), checked or
- * not, and nothing is written.
+ * A workspace without such a plan of these sizes (its max_pages may be smaller) is reported
+ * (MLA_ERR_PLAN_STALE), checked or not, and nothing is written.
  * checked, the status word and every other argument as for mla_decode and mla_decode_fp8.
  */
 size_t mla_shared_workspace_size(const mla_geom* geom, const mla_batch* batch);

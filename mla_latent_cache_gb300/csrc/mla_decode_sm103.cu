@@ -1127,13 +1127,16 @@ __global__ void __launch_bounds__(threads_of<kMode, kForm>(), 1)
   // last), so the walk needs no range count from the header.
   SegWalk walk0(rptr, pair, num_pairs, a.L.cap_ranges);
   if constexpr (kShared) {
-    // A workspace that holds another kind of plan, or one of other sizes, is laid out otherwise:
-    // nothing is attended (asked for with the range pointers, so that it costs no wait of its own).
-    const int4 head = __ldcg(reinterpret_cast<const int4*>(hdr));
+    // A workspace that holds another kind of plan, or one of other sizes, is laid out otherwise, and one for
+    // longer tables has pages past the ends of these: nothing is attended (asked for with the range
+    // pointers, so that it costs no wait of its own, and like them through the L1: every warp asks, which from
+    // the L2 alone took 1.5 of a small batch's 21 us).
+    const int4 head = *reinterpret_cast<const int4*>(hdr);
+    const int kind = hdr[MLA_HDR_CAUSAL], part_o_at = hdr[MLA_HDR_OFF_PART_O],
+              ranges = hdr[MLA_HDR_CAP_RANGES], pages = hdr[MLA_HDR_MAX_PAGES];
     const bool mine = head.x == MLA_PLAN_MAGIC && head.y == a.B && head.z == a.T && head.w == a.H &&
-                      __ldcg(hdr + MLA_HDR_CAUSAL) == kPlanShared + a.causal &&
-                      __ldcg(hdr + MLA_HDR_OFF_PART_O) == (int)a.L.off_part_o &&
-                      __ldcg(hdr + MLA_HDR_CAP_RANGES) == a.L.cap_ranges;
+                      kind == kPlanShared + a.causal && part_o_at == (int)a.L.off_part_o && ranges == a.L.cap_ranges &&
+                      pages <= a.max_pages;
     if (!mine) {
       walk0.num_ranges = 0;
       num_merge_ld = 0;

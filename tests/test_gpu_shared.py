@@ -371,3 +371,28 @@ def test_shared_rows_of_many_parts(mla, cuda, slots, fp8):
         assert s.header()[mla.HDR["PAGES_PER_RANGE"]] == 2       # (71 parts)
         s = Shared(mla, torch, 16, [(2, 64)], [20000, 8000], slots=640, fp8=fp8, seed=slots).run().check()
         assert s.header()[mla.HDR["PAGES_PER_RANGE"]] == 2       # (the fewest: 157 parts)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_plan_for_longer_tables(mla, cuda, fp8):
+    """A plan for tables of more pages than the decode's may have pages past them: nothing is attended.  One for fewer is used."""
+    import torch
+    s = Shared(mla, torch, 16, [(12, 1024)], np.arange(1, 13) * 9, fp8=fp8)
+    own, B = s.batch, s.B
+    s.plan()
+    for pages in (own.max_pages - 1, 1):
+        s.batch = mla.make_batch(B, 1, False, pages)
+        assert mla.mla_shared_workspace_size(s.geom, s.batch) == s.ws_bytes
+        for checked in (0, 1):
+            s.batch = own
+            s.plan()
+            s.batch = mla.make_batch(B, 1, False, pages)
+            s.decode(checked)
+            assert s.status()[0] == mla.MLA_ERR_PLAN_STALE
+        assert bool(torch.isnan(s.o.float()).all()) and bool(torch.isnan(s.lse).all())
+    s.batch = own
+    s.plan()
+    s.batch = mla.make_batch(B, 1, False, own.max_pages + 2)       # (as wide as the table is)
+    s.decode()
+    assert s.status()[0] == mla.MLA_OK
+    s.check()
