@@ -334,6 +334,9 @@ class _PagedLayer:
         out = torch.zeros(B + 1, dtype=torch.bool, device=self.device)
         return out.index_fill_(0, torch.where(stands, d, B), True)[:B]
 
+    def _lose_rows(self, which):
+        """Sequences which (bool [B], on the device) are about to lose the rows that they have."""
+
     def fork(self, src, dst, stream=None):
         """Sequences dst become forks of src (int32 device arrays); what dst held is given back first.  src[f] =
         dst[f] gives the sequence a last page of its own.  A fork that mla_pages_fork refuses (a number
@@ -345,7 +348,9 @@ class _PagedLayer:
         if n > 4096:
             raise ValueError(f"{n} forks")
         with self._on(stream):
-            keep = self.torch.where(self._released(src, dst), 0, self.seq_lens)
+            released = self._released(src, dst)
+            self._lose_rows(released)
+            keep = self.torch.where(released, 0, self.seq_lens)
             copies = self.torch.empty((3, n), dtype=self.torch.int32, device=self.device)
             self._resize(self.seq_lens, keep, self.seq_lens, stream)
             L.check(L.mla_pages_fork(self.refs, self.num_blocks, self.block_table, self.max_pages, self.max_pages,
@@ -511,9 +516,9 @@ class ServeStep(_PagedLayer):
     that a set of sequences shares attended once for all of them, un-absorption.  The rows are the sequence's own from then
     on.  ``sample`` draws the next tokens from the model's logits.  ``fork`` makes sequences of others (samples of one
     prompt, requests behind one system prompt): full pages are shared.  ``set_sharing`` tells which consecutive sequences
-    share how many rows, in up to ``max_sets`` sets (none at first: shared pages are then attended for each sequence); it
-    has to be told anew when a sequence of a set is released or becomes another's fork.  ``release`` gives sequences' pages
-    back.  All of these run on the device without a host synchronisation, so that they can be captured in a CUDA graph
+    share how many rows, in up to ``max_sets`` sets (none at first: shared pages are then attended for each sequence).  A set
+    of which a sequence is released or becomes another's fork shares nothing until it is told anew.  ``release`` gives
+    sequences' pages back.  All of these run on the device without a host synchronisation, so that they can be captured in a CUDA graph
     (but for set_sharing of host arrays).  ``check`` raises what the device reported: the last attention, and everything
     else since the last check.  A sequence whose tokens get no pages (no free block, or past its table) is reported and sits
     the step out: outputs 0, its rows as they were (``live``: the tokens of each sequence that took part).  Arguments that
@@ -556,6 +561,15 @@ class ServeStep(_PagedLayer):
             self.set_ptr[n + 1:] = self.set_ptr[n:n + 1]
             self.prefix_lens[:n].copy_(prefix_lens)
             self.prefix_lens[n:] = 0
+
+    def _lose_rows(self, which):
+        if self.max_sets == 0:
+            return
+        torch = self.torch
+        upto = torch.zeros(self.B + 1, dtype=torch.int64, device=self.device)
+        torch.cumsum(which, 0, out=upto[1:])
+        upto = upto[self.set_ptr.clamp(0, self.B).long()]
+        self.prefix_lens.masked_fill_(upto[1:] > upto[:-1], 0)
 
     def attend(self, q, kv, counts, cos_sin, w_uk, w_uv, q_weight=None, kv_weight=None, eps: float = 1e-6, stream=None):
         """counts int32 [B]: sequence b's tokens are q[b, :counts[b]], kv[b, :counts[b]] (q [B, t, H, 192], kv [B, t, 576],
@@ -631,6 +645,7 @@ class ServeStep(_PagedLayer):
         """The sequences with which[b] (bool [B], on the device) become empty, and their pages are given back."""
         self._fits("which", which, (self.torch.bool,), (self.B,))
         with self._on(stream):
+            self._lose_rows(which)
             self._resize(self.seq_lens, self.torch.where(which, 0, self.seq_lens), self.seq_lens, stream)
 
 

@@ -296,3 +296,48 @@ def test_one_sequence_one_token(mla, cuda):
     for _ in range(66):
         h.step(1, [1])
     h.sample(temperature=0.0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sets_that_lose_members_without_being_told(mla, cuda, fp8):
+    """Members of sets are released and filled with other rows, or become forks of other sequences, and nobody tells the
+    step: what it gives is each sequence's own, eagerly and replayed."""
+    import torch
+    h = Harness(torch, cuda, 66, 16, 350, fp8, seed=23, max_pages=14, num_blocks=330)
+    s = h.s
+    h.step(350, [350, 340] + [0] * 63 + [300])
+    h.step(350, [350, 350] + [0] * 63 + [330])
+    h.fork([0] * 40 + [1] * 23, list(range(2, 42)) + list(range(42, 65)))
+    h.fork([0], [1])                                   # 0 to 41 are samples of one prompt, 42 to 64 of another
+    s.set_sharing([0, 42, 65], [700, 640])
+    h.step(1, [1] * 66)
+    both = h.sets()
+    assert both > 0
+    # a member of the second set ends, and a longer request comes in its place
+    which = torch.zeros(66, dtype=torch.bool, device=cuda)
+    which[50] = True
+    s.release(which)
+    h.rows[50], h.bits[50] = h.rows[50][:0], h.bits[50][:0]
+    h.step(350, [0] * 50 + [350] + [0] * 15)
+    h.step(350, [0] * 50 + [350] + [0] * 15)
+    h.step(1, [1] * 66)
+    assert 0 < h.sets() < both
+    # a member of the first becomes a fork of the other prompt's
+    h.fork([65], [3])
+    h.step(2, [2] * 66)
+    assert h.sets() == 0
+    # told anew, and a release that is replayed
+    s.set_sharing([0, 3, 4, 42], [0, 0, 700])
+    h.step(1, [1] * 66)
+    assert h.sets() > 0
+    which.zero_()
+    s.release(which)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.release(which)
+    which[20] = True
+    g.replay()
+    h.rows[20], h.bits[20] = h.rows[20][:0], h.bits[20][:0]
+    h.step(130, [0] * 20 + [130] + [0] * 45)
+    h.step(1, [1] * 66)
+    assert h.sets() == 0

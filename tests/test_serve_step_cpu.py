@@ -161,3 +161,34 @@ def test_a_vocabulary_past_the_samplings_sums(step, lib):
     assert lib.calls == []
     s.sample(x, (1 << 20) - 1, u=torch.zeros(1))
     assert lib.args["mla_sample"][1] == (1 << 20) - 1
+
+
+def test_a_set_that_loses_a_member_shares_nothing(step, lib):
+    """Released and forked sequences hold other blocks from then on: their sets' prefixes are forgotten, the others' stand."""
+    s = step(B=7, T=8, max_sets=6, num_blocks=30)
+    s.attend(**_inputs(s, 8))
+    release = lambda *b: s.release(torch.tensor([i in b for i in range(7)]))  # noqa: E731
+    fork = lambda src, dst: s.fork(_i32(src), _i32(dst))  # noqa: E731
+    told = [100, 200, 300, 400]
+    for what, args, left in ((release, (), told), (release, (0,), told), (release, (1,), [0, 200, 300, 400]),
+                             (release, (2, 5), [0, 200, 300, 0]), (release, range(7), [0, 200, 0, 0]),
+                             (fork, ([0], [4]), [100, 200, 0, 400]), (fork, ([4, 4], [5, 6]), [100, 200, 300, 0]),
+                             (fork, ([4], [0]), told),
+                             # a last page of its own, and forks that are refused: the rows stay
+                             (fork, ([4], [4]), told), (fork, ([0, 6], [4, 4]), told), (fork, ([-1], [4]), told), (fork, ([0], [7]), told)):
+        s.set_sharing([1, 3, 3, 5, 6], told)          # 1 and 2; none; 3 and 4; 5
+        what(*args)
+        assert s.prefix_lens.tolist() == left + [0, 0], (what, args)
+        assert s.set_ptr.tolist() == [1, 3, 3, 5, 6, 6, 6]
+    none = step(max_sets=0)
+    none.release(torch.tensor([True, False, True]))
+
+
+def test_bounds_that_leave_the_batch_keep_no_set(step, lib):
+    """Bounds on the device are not looked at on the host; the plan reports them, and release does not go by them."""
+    s = step(B=3, max_sets=3)
+    s.set_sharing(_i32([-5, 2, 1 << 30]), _i32([64, 64]))
+    s.release(torch.tensor([False, True, False]))
+    assert s.prefix_lens.tolist() == [0, 64, 0]
+    s.release(torch.tensor([False, False, True]))
+    assert s.prefix_lens.tolist() == [0, 0, 0]
