@@ -297,7 +297,9 @@ mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, con
  *     prefix_lens[p] rows (int32 [num_sets]).  What they share is cut to whole pages that
  *     every query token of the set's sequences sees; what is longer is attended with each
  *     sequence's own rows.  The blocks are read through the table row of the set's first
- *     sequence that is not empty.  A set whose sharing does not save work is attended like
+ *     sequence that is not empty; a sequence with tokens whose own row has another block at the
+ *     last shared page (checked: at any of them) is reported (MLA_ERR_DEVICE_CHECK, info = the
+ *     sequence), checked or not, and its tokens see the rows behind the shared ones alone.  A set whose sharing does not save work is attended like
  *     unshared sequences (T * H a multiple of 128: always; results differ by rounding alone).
  *     num_sets 0 (the arrays NULL): nothing is shared.
  *   q_lens int32 [B] (NULL: T each): sequence b has q_lens[b] query tokens, 0 <= q_lens[b] <=

@@ -236,6 +236,10 @@ struct FastArgs {
   WsLayout L;
 };
 
+__device__ __forceinline__ merge::Tables merge_tables(const FastArgs& a) {
+  return {a.block_table, a.bt_stride, a.seq_lens, a.node_lens, a.T, a.T * a.H, a.max_rows, a.checked};
+}
+
 struct Shared {
   uint32_t base;
   __device__ uint32_t q(int box) const { return base + kSmemQ + (box - kQTmemBoxes) * kQBoxBytes; }
@@ -1270,7 +1274,7 @@ __global__ void __launch_bounds__(threads_of<kMode, kForm>(), 1)
     if constexpr (kShared) {
       const int records = walk0.num_ranges > 0 ? __ldcg(hdr + MLA_HDR_NUM_MERGE) : 0;
       const merge::Slots slots(records, R, blockIdx.x, gridDim.x);
-      if (slots.first < slots.end) merge::look_up(reinterpret_cast<merge::Share*>(smem + kSmemShares), ws, a.L, slots, slots.first);
+      if (slots.first < slots.end) merge::look_up(reinterpret_cast<merge::Share*>(smem + kSmemShares), ws, a.L, slots, slots.first, merge_tables(a));
     }
     __syncwarp();
   } else if (kQueryWarps && warp >= 12) {
@@ -1592,7 +1596,8 @@ __global__ void __launch_bounds__(threads_of<kMode, kForm>(), 1)
     if constexpr (kShared)
       merge::merge_shared_share<threads_of<kMode, kForm>() / 128>(out, ws, a.L, num_merge, blockIdx.x, gridDim.x,
                                                                   reinterpret_cast<float*>(smem + kSmemRing),
-                                                                  reinterpret_cast<merge::Share*>(smem + kSmemShares), *reinterpret_cast<merge::Staged*>(smem + kSmemQ));
+                                                                  reinterpret_cast<merge::Share*>(smem + kSmemShares),
+                                                                  *reinterpret_cast<merge::Staged*>(smem + kSmemQ), merge_tables(a));
     else
       merge::merge_plan_share<threads_of<kMode, kForm>() / 128>(out, ws, a.L, num_merge, blockIdx.x, gridDim.x,
                                             reinterpret_cast<float*>(smem + kSmemRing), s_merge_ok);

@@ -32,13 +32,14 @@ __device__ __forceinline__ Parts parts_of(const int* grp, int g) {
 struct RowParts {
   Parts own, set0, set1;    // set1: the set's next group (k = 0 where the rows end before it)
   int first_row, rows, place;
+  bool foreign;             // the sequence does not hold the set's pages: the set's parts are not its own
   // The partial row of part r of the record's row i, or -1.
   __device__ __forceinline__ long long at(int i, int r) const {
     if (r < own.k) return own.base + (long long)r * own.rows + i;
     const int j = r - own.k, p = place + i;
     const bool next = p >= kRowsPerBlock;
     const int k = next ? set1.k : set0.k;
-    if (j >= k) return -1;
+    if (j >= k || foreign) return -1;
     return next ? set1.base + (long long)j * set1.rows + (p - kRowsPerBlock) : set0.base + (long long)j * set0.rows + p;
   }
   __device__ __forceinline__ int most() const { return own.k + max(set0.k, set1.k); }
@@ -140,7 +141,7 @@ __device__ __forceinline__ void merge_shared_row(const Out& a, const float* part
     const size_t r0 = p.at(row, 0);
     fold_partials(st, part_o + r0 * kDLat + c, part_lse + r0, (size_t)p.own.rows * kDLat, p.own.rows, grp, G, p.own.k);
   }
-  if (set_of.k > 0) {
+  if (set_of.k > 0 && !p.foreign) {
     const size_t r0 = p.at(row, p.own.k);
     fold_partials(st, part_o + r0 * kDLat + c, part_lse + r0, (size_t)set_of.rows * kDLat, set_of.rows, grp, G, set_of.k);
   }
@@ -209,8 +210,31 @@ struct Slots {
   __device__ __forceinline__ int count(long long v) const { return (int)(min(end, (record(v) + kRecords) * per_rec) - v); }
 };
 
+// What tells whether the sequences of a set hold the same pages.
+struct Tables {
+  const int32_t* block_table;
+  int stride;
+  const int32_t *seq_lens, *q_lens;
+  int T, R, max_rows, checked;
+};
+// Whether sequence b, which has query tokens, holds other blocks than table row `read` in its first `pages`
+// pages.  Forks share leading pages, so that the last page tells; checked, all are compared.
+__device__ __forceinline__ bool holds_others(const Tables& t, int b, int read, int pages) {
+  const int S = t.seq_lens[b];
+  if (b == read || tree_nodes(t.q_lens, b, t.T, S < 0 ? 0 : min(S, t.max_rows)) == 0) return false;
+  const int32_t* const mine = t.block_table + (size_t)b * t.stride;
+  const int32_t* const his = t.block_table + (size_t)read * t.stride;
+  bool others = mine[pages - 1] != his[pages - 1];
+  for (int p = 0; t.checked && p < pages - 1; ++p) others = others || mine[p] != his[p];
+  return others;
+}
+
 // The records of the slots from v on, and their groups, to shares[]: one warp, four lanes to a record.
-__device__ __forceinline__ void look_up(Share* shares, const char* ws, const WsLayout& L, const Slots& slots, long long v) {
+// A sequence that does not hold the pages of its set is reported, and gets none of the set's parts: what
+// was attended there are somebody else's rows.  (Looked at here, while the pages are attended: by
+// the softmax warps, at each segment, it cost documents 105 -> 117 us.)
+__device__ __forceinline__ void look_up(Share* shares, char* ws, const WsLayout& L, const Slots& slots, long long v,
+                                        const Tables& tables) {
   const int* grps = reinterpret_cast<const int*>(ws + L.off_groups);
   const int* mrg = reinterpret_cast<const int*>(ws + L.off_merge);
   const int i = (threadIdx.x & 31) / 4, which = threadIdx.x % 4;
@@ -225,6 +249,10 @@ __device__ __forceinline__ void look_up(Share* shares, const char* ws, const WsL
     s.p.first_row = first_row;
     s.p.rows = rows;
     s.p.place = place;
+    const int b = first_row / tables.R;
+    s.p.foreign = set >= 0 && holds_others(tables, b, __ldcg(grps + (size_t)set * kSharedGroupWords + 5),
+                                           __ldcg(grps + (size_t)own * kSharedGroupWords + 1));
+    if (s.p.foreign) record_error(reinterpret_cast<int*>(ws), MLA_ERR_DEVICE_CHECK, b);
     s.row_a = i == 0 ? slot : 0;
     s.row_b = min(rows, slot + nslots - i * slots.per_rec);
   } else {
@@ -240,7 +268,7 @@ __device__ __forceinline__ void look_up(Share* shares, const char* ws, const WsL
 // two to three parts each.
 template <int G>
 __device__ __forceinline__ void merge_shared_share(const Out& a, char* ws, const WsLayout& L, int num_merge, int cta,
-                                                   int nctas, float* s_st, Share* shares, Staged& st) {
+                                                   int nctas, float* s_st, Share* shares, Staged& st, const Tables& tables) {
   int* hdr = reinterpret_cast<int*>(ws);
   int* msync = reinterpret_cast<int*>(ws + L.off_merge_sync);
   const float* part_lse = reinterpret_cast<const float*>(ws + L.off_part_lse);
@@ -250,7 +278,7 @@ __device__ __forceinline__ void merge_shared_share(const Out& a, char* ws, const
   const int t = threadIdx.x % (kDLat / 4);
   for (long long v = slots.first; v < slots.end;) {
     if (v > slots.first) {
-      if (threadIdx.x < 32) look_up(shares, ws, L, slots, v);
+      if (threadIdx.x < 32) look_up(shares, ws, L, slots, v, tables);
       __syncthreads();
     }
     const int slot = (int)(v - slots.record(v) * slots.per_rec), nslots = slots.count(v);

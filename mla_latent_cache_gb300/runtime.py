@@ -517,8 +517,9 @@ class ServeStep(_PagedLayer):
     on.  ``sample`` draws the next tokens from the model's logits.  ``fork`` makes sequences of others (samples of one
     prompt, requests behind one system prompt): full pages are shared.  ``set_sharing`` tells which consecutive sequences
     share how many rows, in up to ``max_sets`` sets (none at first: shared pages are then attended for each sequence).  A set
-    of which a sequence is released or becomes another's fork shares nothing until it is told anew.  ``release`` gives
-    sequences' pages back.  All of these run on the device without a host synchronisation, so that they can be captured in a CUDA graph
+    of which a sequence is released or becomes another's fork shares nothing until it is told anew.  A set may be told with
+    empty sequences in it; once one of them has rows of its own it has to be told anew (a sequence that holds other rows than
+    its set is reported, and does not see the set's).  ``release`` gives sequences' pages back.  All of these run on the device without a host synchronisation, so that they can be captured in a CUDA graph
     (but for set_sharing of host arrays).  ``check`` raises what the device reported: the last attention, and everything
     else since the last check.  A sequence whose tokens get no pages (no free block, or past its table) is reported and sits
     the step out: outputs 0, its rows as they were (``live``: the tokens of each sequence that took part).  Arguments that

@@ -341,3 +341,29 @@ def test_sets_that_lose_members_without_being_told(mla, cuda, fp8):
     h.step(130, [0] * 20 + [130] + [0] * 45)
     h.step(1, [1] * 66)
     assert h.sets() == 0
+
+
+def test_an_empty_member_that_begins_anew_is_reported(mla, cuda):
+    import torch
+    h = Harness(torch, cuda, 40, 16, 350, seed=27, max_pages=14, num_blocks=200)
+    s = h.s
+    for _ in range(2):
+        h.step(350, [350] + [0] * 39)
+    h.fork([0] * 38, list(range(1, 39)))
+    s.set_sharing([0, 40], [700])                        # (the last one is empty)
+    h.step(1, [1] * 39 + [0])
+    assert h.sets() > 0
+    h.step(350, [0] * 39 + [350])                        # its first rows: nothing is shared beside them
+    for t in (350, 1):
+        h.draw_inputs(t, [1] * 39 + [t])
+        h.attend()
+    torch.cuda.synchronize()
+    with pytest.raises(mla.MlaError, match=r"\(39\)"):
+        s.check()
+    # told anew, all is as it should be
+    s.set_sharing([0, 39], [700])
+    h.draw_inputs(1, [1] * 40)
+    h.attend()
+    torch.cuda.synchronize()
+    s.check()
+    assert h.sets() > 0

@@ -396,3 +396,50 @@ def test_a_plan_for_longer_tables(mla, cuda, fp8):
     s.decode()
     assert s.status()[0] == mla.MLA_OK
     s.check()
+
+
+def _decode_rows(s, b, first):
+    """Sequence b's tokens over its rows from `first` on."""
+    f = s.torch.nan_to_num(s.q).double().numpy()[b:b + 1]
+    k = int(s.lens[b]) - first
+    blocks = s.bt[b:b + 1, first // 64:]
+    return O.ragged_decode_ref(f[..., :512], f[..., 512:], s.f64, blocks, [k], s.counts[b:b + 1], s.causal)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,T", [(16, 1), (16, 3), (64, 1), (64, 3)])
+def test_members_that_hold_other_blocks(mla, cuda, H, T, fp8):
+    """A sequence in a set that does not hold the set's blocks is reported, checked or not, and sees none of them."""
+    import torch
+    sets, own = [(30, 4096)], np.concatenate([np.arange(30) * 5 + 4, [4500]])
+    for odd, causal in (((3,), False), ((0, 8, 29), True)):
+        s = Shared(mla, torch, H, sets, own, T, None, causal, fp8=fp8, slots=16)
+        s.bt[list(odd), :64] = s.bt[30, :64]              # (the loose sequence's)
+        s.d_bt.copy_(torch.from_numpy(s.bt))
+        # through the table row of the first: if that one is odd, it is the others that hold other blocks
+        alone = [b for b in range(30) if (s.bt[b, :64] != s.bt[0, :64]).any()]
+        assert len(alone) == (1 if 0 not in odd else 27)
+        ro, rl = O.ragged_decode_ref(*(torch.nan_to_num(s.q).double().numpy()[..., i:j] for i, j in ((0, 512), (512, 576))), s.f64, s.bt,
+                                     s.lens, s.counts, causal)
+        for b in alone:
+            (ro[b],), (rl[b],) = _decode_rows(s, b, 4096)
+        for checked in (0, 1):
+            s.o.fill_(float("nan"))
+            s.plan()
+            assert s.set_groups() > 0
+            s.decode(checked)
+            status, info = s.status()
+            assert status == mla.MLA_ERR_DEVICE_CHECK and info in alone
+            parity(_np(s.o), ro, "o_lat")
+            parity(_np(s.lse), rl, "lse")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_other_block_among_the_shared(mla, cuda, fp8):
+    """Checked, every page of a member is compared with the one that is read."""
+    import torch
+    for page in (0, 13, 31):
+        s = Shared(mla, torch, 16, [(30, 2048)], np.arange(30) * 5 + 4, slots=16, fp8=fp8)
+        s.d_bt[17, page] = int(s.bt[2, 32])
+        s.run(expect=mla.MLA_ERR_DEVICE_CHECK)
+        assert s.set_groups() > 0 and s.status()[1] == 17
