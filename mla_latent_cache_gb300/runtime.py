@@ -611,8 +611,8 @@ class ServeStep(_PagedLayer):
         return self.o.view(-1)[:N * self.H * 128].view(self.B, T, self.H, 128)
 
     def sample(self, logits, V: int, u=None, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, stream=None):
-        """The next token of each row of logits [N, >= V] (fp32 or bf16; mla_sample's rule) -> int32 [N] (u None: none);
-        probs [N, >= V], fp32 or bf16: the probabilities that the filters leave."""
+        """The next token of each row of logits [N, >= V] (fp32 or bf16; mla_sample's rule) -> int32 [N] (u None: none), a
+        new tensor each time (``tokens``: the last one); probs [N, >= V], fp32 or bf16: the probabilities that the filters leave."""
         torch = self.torch
         types = (torch.float32, torch.bfloat16)
         dtype = lambda t: L.MLA_DTYPE_BF16 if t.dtype == torch.bfloat16 else L.MLA_DTYPE_F32  # noqa: E731
@@ -637,9 +637,11 @@ class ServeStep(_PagedLayer):
             if t is not None:
                 self._fits(name, t, (kind,), (N,))
         with self._on(stream):
-            tokens = None if u is None else self.tokens if N == self.B else torch.empty(N, dtype=torch.int32, device=self.device)
+            tokens = None if u is None else torch.empty(N, dtype=torch.int32, device=self.device)
             L.check(L.mla_sample(N, V, logits, dtype(logits), step, temperature, top_k, top_p, min_p, u, tokens, probs,
                                  L.MLA_DTYPE_F32 if probs is None else dtype(probs), probs_step, stream), "mla_sample")
+        if tokens is not None:
+            self.tokens = tokens
         return tokens
 
     def release(self, which, stream=None):

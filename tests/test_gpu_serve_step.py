@@ -367,3 +367,25 @@ def test_an_empty_member_that_begins_anew_is_reported(mla, cuda):
     torch.cuda.synchronize()
     s.check()
     assert h.sets() > 0
+
+
+def test_draws_do_not_overwrite_one_another(mla, cuda):
+    """Two settings on the same logits, a captured draw among them: each keeps its own tokens."""
+    import torch
+    h = Harness(torch, cuda, 9, 16, 1, seed=29, max_pages=1)
+    s = h.s
+    x = torch.from_numpy(h.rng.standard_normal((9, h.V))).float().to(cuda)
+    low, high = torch.zeros(9, device=cuda), torch.full((9,), 1 - 2.0 ** -24, device=cuda)
+    first, last = x.argmax(1).tolist(), x.argmin(1).tolist()
+    a = s.sample(x, h.V, u=low)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c = s.sample(x, h.V, u=high)
+    b = s.sample(x, h.V, u=high)
+    g.replay()
+    d = s.sample(x, h.V, u=low)
+    assert (a.tolist(), b.tolist(), c.tolist(), d.tolist()) == (first, last, last, first) and s.tokens is d
+    low.fill_(1 - 2.0 ** -24)
+    high.zero_()
+    g.replay()
+    assert (a.tolist(), b.tolist(), c.tolist(), d.tolist()) == (first, last, first, first)

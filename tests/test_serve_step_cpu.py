@@ -192,3 +192,19 @@ def test_bounds_that_leave_the_batch_keep_no_set(step, lib):
     assert s.prefix_lens.tolist() == [0, 64, 0]
     s.release(torch.tensor([False, False, True]))
     assert s.prefix_lens.tolist() == [0, 0, 0]
+
+
+def test_tokens_of_an_earlier_draw_stay(step, lib):
+    s = step(B=3)
+    x = torch.zeros(3, 104)
+    draws = []
+    for i in range(3):
+        draws.append(s.sample(x, 101, u=torch.zeros(3)))
+        assert lib.args["mla_sample"][10] is draws[-1] is s.tokens
+        draws[-1].fill_(i)
+    assert [d.tolist() for d in draws] == [[0] * 3, [1] * 3, [2] * 3]
+    assert s.sample(x, 101, probs=torch.zeros(3, 104)) is None and s.tokens is draws[2]
+    lib.answers["mla_sample"] = -6
+    with pytest.raises(Exception):
+        s.sample(x, 101, u=torch.zeros(3))
+    assert s.tokens is draws[2]
