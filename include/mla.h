@@ -299,8 +299,9 @@ mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, con
  *     sequence's own rows.  The blocks are read through the table row of the set's first
  *     sequence that is not empty; a sequence with tokens whose own row has another block at the
  *     last shared page (checked: at any of them) is reported (MLA_ERR_DEVICE_CHECK, info = the
- *     sequence), checked or not, and its tokens see the rows behind the shared ones alone.  A set whose sharing does not save work is attended like
- *     unshared sequences (T * H a multiple of 128: always; results differ by rounding alone).
+ *     sequence), checked or not, and its tokens see the rows behind the shared ones alone.  A set
+ *     whose sharing does not save work is attended like unshared sequences (T * H a multiple of
+ *     128, or chunks of prompts behind tables of few pages: always; results differ by rounding alone).
  *     num_sets 0 (the arrays NULL): nothing is shared.
  *   q_lens int32 [B] (NULL: T each): sequence b has q_lens[b] query tokens, 0 <= q_lens[b] <=
  *     min(T, S_b) unless S_b = 0: tokens t < q_lens[b] at [b, t]; with causal != 0 they are
@@ -309,8 +310,8 @@ mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, con
  *     not matter, NaN neither).
  *   batch: B <= 8192, T, causal, max_pages, num_slots and num_splits_override as for mla_decode.
  * mla_plan_shared stands in for mla_plan, with a workspace of mla_shared_workspace_size()
- * bytes (0 on invalid arguments; two fp32 rows of 512 per query row, beside the tables), and
- * is re-run when lengths, query tokens, sets or prefixes change.  The split rule is
+ * bytes (0 on invalid arguments; beside the tables, two fp32 rows of 512 per query row where a
+ * set can save work with these T, H and max_pages, else some per slot), and is re-run when lengths, query tokens, sets or prefixes change.  The split rule is
  * mla_plan's, with ranges of at least 2 pages, over the sets' groups (128 query rows of the
  * set's sequences, one behind the other) and then the sequences'.  Its records: segment
  * int32[8] = {table row, first query row in [B T H], page_begin, page_end, range, first partial
@@ -318,8 +319,8 @@ mla_status mla_decode_tree_fp8(const mla_geom* geom, const mla_batch* batch, con
  * take a row per query row of their group; the plan header's MLA_HDR_CAUSAL word is 4 + causal,
  * MLA_HDR_NUM_PARTIALS and MLA_HDR_CAP_PARTIALS count partial rows.  Sets that do not rise or
  * leave the batch, and negative prefixes, are reported (info = B), and nothing is shared.
- * A workspace without such a plan of these sizes (its max_pages may be smaller) is reported
- * (MLA_ERR_PLAN_STALE), checked or not, and nothing is written.
+ * A workspace without such a plan of these sizes is reported (MLA_ERR_PLAN_STALE), checked or
+ * not, and nothing is written.
  * checked, the status word and every other argument as for mla_decode and mla_decode_fp8.
  */
 size_t mla_shared_workspace_size(const mla_geom* geom, const mla_batch* batch);

@@ -87,19 +87,21 @@ bool compute_layout(const mla_geom* g, const mla_batch* b, WsLayout* L) {
   return true;
 }
 
-// A shared plan's workspace.  Sets of 128-row multiples share nothing (their rows fill as many
-// groups either way); of the others, every row has a part of its set's pages and one of its
-// sequence's own, and each range may cut a group once more.
+// A shared plan's workspace.  Where no set can save anything (rows that are multiples of 128, and chunks
+// of prompts behind short prefixes), it is the plain plan's; else every row has a part of its set's pages
+// and one of its sequence's own, and each range may cut a group once more.  (64 sequences x 16 heads with
+// chunks of up to 1023 tokens and tables of 512 pages: 4.3 GB if all could share, 0.87 GB.)
 bool compute_shared_layout(const mla_geom* g, const mla_batch* b, WsLayout* L) {
   const long long R = (long long)b->T * g->H, RB = (R + kRowsPerBlock - 1) / kRowsPerBlock;
-  const long long own = b->B * RB, groups = R % kRowsPerBlock == 0 ? own : 2 * own;
+  const bool shares = may_share(R, b->max_pages);
+  const long long own = b->B * RB, groups = shares ? 2 * own : own;
   const int G = resolve_slots(b);
   long long cap_ranges = G, cap_segments = groups + G;
-  long long rows = R % kRowsPerBlock == 0 ? 2LL * G * kRowsPerBlock : 2 * b->B * R + (long long)G * kRowsPerBlock;
+  long long rows = shares ? 2 * b->B * R + (long long)G * kRowsPerBlock : 2LL * G * kRowsPerBlock;
   if (b->num_splits_override > 0) {
     const long long k = b->num_splits_override < b->max_pages ? b->num_splits_override : b->max_pages;
     cap_ranges = cap_segments = groups * k;
-    rows = (R % kRowsPerBlock == 0 ? 1 : 2) * b->B * R * k;
+    rows = (shares ? 2 : 1) * b->B * R * k;
   }
   if (cap_segments > (1 << 26) || (long long)b->B * R >= (1LL << 31) || rows >= (1LL << 31)) return false;
   size_t off = align_up(MLA_HDR_WORDS * sizeof(int));

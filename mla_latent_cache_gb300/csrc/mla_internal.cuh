@@ -118,6 +118,18 @@ struct SharedSets {
 };
 constexpr int kPlanShared = 4;                  // a shared plan's MLA_HDR_CAUSAL, plus its causal flag
 constexpr int kMaxSharedSequences = 8192;
+// What sharing costs a set, in pages (measured beside the planner): per group of 128 rows, and for so many
+// rows of the set once more per group.
+constexpr int kSharedGroupCost = 2, kSharedRowsPerPage = 384;
+// Whether any set can save by sharing, with R query rows per sequence and tables of so many pages.  m members
+// save (m RB - g) pages - (2 + floor(m R / 384)) g, RB = ceil(R / 128) and g = ceil(m R / 128) >= m R / 128: more
+// than nothing only if (128 RB - R) pages > (1 + m R / 384) R.  One member alone saves nothing (g = RB), more of
+// them make the right side larger.  (R a multiple of 128: its rows fill as many groups either way.)
+__host__ __device__ __forceinline__ bool may_share(long long R, long long pages) {
+  static_assert(kSharedGroupCost == 2, "2 + floor(x) > 1 + x");
+  const long long spare = (kRowsPerBlock - R % kRowsPerBlock) % kRowsPerBlock;
+  return spare * pages * kSharedRowsPerPage > (kSharedRowsPerPage + 2 * R) * R;
+}
 // A shared plan's group record: (pages, first page, segments, first segment), (first row of the
 // partial states, or -1: final; table row; first query row in [B, T, H]; rows | set's flag << 16),
 // (line position and the first gap, non-empty groups before, the gap ahead of it, 0).

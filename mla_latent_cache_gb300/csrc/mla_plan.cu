@@ -365,8 +365,7 @@ __device__ __forceinline__ int shared_gap(int rows) { return min(2 + rows / 8, 8
 //   48 x 64 heads, prefix 512: 27.6 and 25.8; 1536: 31.5 and 36.2; 12000: 80 and 127
 //   96 x 3 tokens x 64 heads, prefix 4096: 208 and 171; 48 of those, 4096: 104 and 95; 12000: 215 and 219
 // Of 79 such batches (4 to 96 sequences, prefixes of 512 to 12000) the rule takes the faster way, or one that is
-// within 5 % of it.
-constexpr int kSharedGroupCost = 2, kSharedRowsPerPage = 384;    // per group, and one more for so many rows of the set
+// within 5 % of it (kSharedGroupCost, kSharedRowsPerPage).
 constexpr int kSharedLeastSaved = 1;                             // pages per range, over all sets
 
 struct SharedPlanArgs {
@@ -465,12 +464,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(SharedPlanArg
   }
   __syncthreads();
 
-  // What each set shares: whole pages, and only where that pays.  (A set of 128-row multiples
-  // saves nothing: its rows fill as many groups either way.)
+  // What each set shares: whole pages, and only where that pays (the workspace is laid out for what can).
   int saved_all = 0;
   for (int p = tid; p < P; p += blockDim.x) {
     int pages = 0;
-    if (sets > 0 && s_pages[p] != INT_MAX) {
+    if (sets > 0 && s_pages[p] != INT_MAX && may_share(R, a.max_pages)) {
       const long long members = s_ptr[p + 1] - s_ptr[p], rows = members * R;
       const long long groups = (rows + kRowsPerBlock - 1) / kRowsPerBlock;
       pages = min(s_pages[p], a.prefix_lens[p]) / kPage;

@@ -443,3 +443,14 @@ def test_one_other_block_among_the_shared(mla, cuda, fp8):
         s.d_bt[17, page] = int(s.bt[2, 32])
         s.run(expect=mla.MLA_ERR_DEVICE_CHECK)
         assert s.set_groups() > 0 and s.status()[1] == 17
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("pages,shares", [(6, False), (20, False), (24, False), (29, False), (60, True), (200, True)])
+def test_chunks_of_prompts_in_sets(mla, cuda, pages, shares, fp8):
+    """Two sequences of 41 tokens x 16 heads each (656 rows): sharing saves one group of twelve, and costs 55 pages; tables of
+    25 pages or fewer are laid out without it."""
+    import torch
+    s = Shared(mla, torch, 16, [(2, 64 * pages)], [50, 41, 3000 if pages == 20 else 60], 41, [41, 30, 41], True, fp8=fp8, slots=2)
+    s.run().covered().check()
+    assert (s.set_groups() > 0) == shares

@@ -113,3 +113,26 @@ def test_sample_vocabularies_whose_sums_do_not_fit(mla):
                                                k=None, p=None, mp=None, u=0x60000, tokens=0x70000, probs=None, pd=0, ps=0))
     assert call() == mla.MLA_ERR_SHAPE and call(N=2) == mla.MLA_ERR_SHAPE
     assert call(V=(1 << 20) - 1) == mla.MLA_OK
+
+
+def test_shared_workspace_of_what_can_share(mla):
+    """Chunks of prompts that no set can save anything of need no partial states for sharing."""
+    import numpy as np
+    from oracle import serve_oracle as S
+    size = lambda B, T, H, pages, **kw: mla.mla_shared_workspace_size(mla.make_geom(H), mla.make_batch(B, T, True, pages, num_slots=8, **kw))  # noqa: E731
+    row = 512 * 4 + 4
+    cuts = 2 * 8 * 128 * row
+    assert size(64, 1023, 16, 64) < cuts + (4 << 20)
+    assert size(64, 1, 16, 1) >= 2 * 64 * 16 * row          # a page is enough for samples
+    assert size(64, 1023, 16, 64, num_splits_override=4) < 1.01 * 4 * 64 * 1023 * 16 * row + (16 << 20)
+    # what can share by the planner's rule, for any number of members, has a part for every row twice
+    rng = np.random.default_rng(0)
+    seen = set()
+    for _ in range(300):
+        H, T, pages, m = (int(v) for v in (rng.choice([1, 8, 16, 64, 128]), 2 ** rng.uniform(0, 9), 2 ** rng.uniform(0, 12),
+                                           rng.integers(2, 40)))
+        shares = S.shared_pages_ref([64 * pages] * m, [T] * m, [0, m], [64 * pages], T, H, False, 0) != [0]
+        seen.add(shares)
+        if shares:
+            assert size(m, T, H, pages) >= 2 * m * T * H * row, (H, T, pages, m)
+    assert seen == {False, True}
