@@ -454,3 +454,26 @@ def test_chunks_of_prompts_in_sets(mla, cuda, pages, shares, fp8):
     s = Shared(mla, torch, 16, [(2, 64 * pages)], [50, 41, 3000 if pages == 20 else 60], 41, [41, 30, 41], True, fp8=fp8, slots=2)
     s.run().covered().check()
     assert (s.set_groups() > 0) == shares
+
+
+def test_members_of_many_that_hold_other_blocks(mla, cuda):
+    """As above where a CTA merges more records than it looks up at once, by a thousand and five hundred sequences."""
+    import torch
+    rng = np.random.default_rng(6)
+    B = 1500
+    s = Shared(mla, torch, 8, [(10, 700)] * 140, rng.integers(1, 40, B))
+    odd = [b for b in range(3, 1400, 97) if b % 10]
+    for b in odd:
+        s.bt[b, :10] = s.bt[(b + 500) % 1400, :10]            # (another set's)
+    s.d_bt.copy_(torch.from_numpy(s.bt))
+    f = torch.nan_to_num(s.q).double().numpy()
+    ro, rl = O.ragged_decode_ref(f[..., :512], f[..., 512:], s.f64, s.bt, s.lens, s.counts, False)
+    for b in odd:
+        (ro[b],), (rl[b],) = _decode_rows(s, b, 640)
+    s.plan()
+    assert s.set_groups() > 0
+    s.decode(0)
+    status, info = s.status()
+    assert status == mla.MLA_ERR_DEVICE_CHECK and info in odd
+    parity(_np(s.o), ro, "o_lat")
+    parity(_np(s.lse), rl, "lse")
