@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a, char* ws
 // Small segments change sooner (16 rows ~3.5 us, 32 ~5, 128 ~7, the partial states' stores among it; a page
 // 0.87).  Plan and decode of samples of a prompt (own groups of 16 rows), documents (32) and 40 FP8 sequences (128
 // and 64) in us: 8 for all 38.1, 104, 74.4; 4 for all 36.6, 119, 75.8; 4 + rows / 32 35.4, 109, 75.6; this 34.5, 103,
-// 74.6.  The plan itself takes 5.4 to 6.2 us, a chain of dependent loads and block scans (10 behind a decode that
+// 74.6.  (On those three batches; on no others.)  The plan itself takes 5.4 to 6.2 us, a chain of dependent loads and block scans (10 behind a decode that
 // has emptied the L2 of its code).
 __device__ __forceinline__ int shared_gap(int rows) { return min(2 + rows / 8, 8); }
 // Sharing a set's pages costs a segment per 128 of its rows and the partial states of all of

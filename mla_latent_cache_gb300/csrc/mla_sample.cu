@@ -26,10 +26,10 @@
 //
 // What bounds it: 82 instructions a token of a row with a histogram of masses (issued on every cycle:
 // 129280 tokens of 32 rows take 21 of 60 thousand cycles), and for every row 14 to 20
-// thousand cycles of phases that wait for one another: the first loads, six barriers of the
+// thousand cycles of phases that wait for one another: the first loads, five barriers of the
 // cluster, instructions that are fetched to be run once.  Measured: one bf16 row of 32000, top-k
-// and top-p, 10.9 us; 64 fp32 rows of 129280 with mixed settings 38 us; 32 of them without filters 31 us; 96 rows
-// of 50257 with top-p and their probabilities 51 us.  (A first form, which sorted nothing either but took
+// and top-p, 9.0 us; 64 fp32 rows of 129280 with mixed settings 41 us; 32 of them without filters 31 us; 96 rows
+// of 50257 with top-p and their probabilities 50 us.  (A first form, which sorted nothing either but took
 // double precision, one CTA a row and a pass per border: 611, 3015, 1823, 1230 us.)
 #include <limits.h>
 #include <math.h>
